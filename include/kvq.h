@@ -93,6 +93,12 @@ extern "C" {
 #define KVQ_FLAG_BAD_PAGE     1u  /* a page-table entry outside [0, num_pages) */
 #define KVQ_FLAG_BAD_SEQLEN   2u  /* seq_len < 0, > max_seq_len or > max_pages*page_size */
 #define KVQ_FLAG_TIMEOUT      4u  /* a bounded wait (cross-CTA exchange, flag) gave up */
+#define KVQ_FLAG_NO_PAGES     8u  /* kvq_plan_step: fewer free pages than the step needs */
+#define KVQ_FLAG_NO_SLOTS    16u  /* kvq_plan_step: more new tokens than max_tokens */
+
+/* Element types of an output (kvq_prompt_attn, kvq_prefix_attn). */
+#define KVQ_OUT_F32 0
+#define KVQ_OUT_F16 1
 
 /* Compile-time limits of the library. */
 #define KVQ_MAX_GROUP        8     /* query heads per KV head (num_q_heads / num_kv_heads) */
@@ -122,8 +128,9 @@ size_t kvq_scale_row_count(int32_t fmt, int32_t head_dim);
  *   Walsh-Hadamard-rotated codebook KV formats the method runs on) and "Ключевые выводы"
  *   (NVFP4); the pages fix no block arithmetic, so the formulas above are this library's.
  *   x       device fp16 [n_tokens][num_kv_heads][head_dim]
- *   slots   device int32 [n_tokens]: physical slot of token i (NULL: slot i);
- *           every slot must lie in [0, num_pages*page_size) (not checked on device)
+ *   slots   device int32 [n_tokens]: physical slot of token i (NULL: slot i); a negative
+ *           slot skips its token (the padding that kvq_plan_step writes); every other
+ *           slot must lie in [0, num_pages*page_size) (not checked on device)
  *   codes, scales  device planes (layout above), 16-byte aligned
  * The block formulas are the ones in the header comment; the result is
  * bit-identical to an IEEE fp32 evaluation of them.  lut4 needs desc->codebook
@@ -308,6 +315,118 @@ int kvq_decode_attn_noalloc(const kvq_cache_desc* desc, const void* q, int32_t b
  * KVQ_ERR_INVALID_ARG for a null `flags`, KVQ_ERR_CUDA if a CUDA call fails.
  */
 int kvq_noalloc_read_flags(uint32_t* flags, void* stream);
+
+/*
+ * kvq_plan_step -- the page bookkeeping of one serving step, on the device: the page table,
+ * slot map, positions and offsets that kvq_quantize_kv, kvq_prompt_attn, kvq_prefix_attn and
+ * kvq_decode_attn take, from the lengths of the requests.
+ *   (No passage: the pages assume a filled cache.)
+ *   batch        requests, 0..KVQ_MAX_BATCH
+ *   seq_lens     device int32 [batch]: positions in the cache, n_b
+ *   new_lens     device int32 [batch]: tokens to append, a_b >= 0; -1: the request ends
+ *   free_pages   device int32 [num_pages]: a stack of unused pages, the first *free_count
+ *                entries.  The pages of the ended requests (request order, page order) are
+ *                pushed; then the j-th page that the step needs (request order, page order)
+ *                is popped: with F the stack after the pushes, page j = F[|F| - 1 - j].
+ *                Entries above the count may be overwritten.
+ *   free_count   device int32 [1]
+ *   page_table   device int32 [batch][max_pages]: the first ceil(n_b / page_size) entries of
+ *                row b are its pages; the new pages are written behind them.  Nothing else
+ *                of the table changes.
+ *   seq_lens_out   device int32 [batch]: n_b + a_b, 0 for an ended request (may be seq_lens)
+ *   free_count_out device int32 [1]: the stack's height afterwards (may be free_count)
+ *   token_offsets  device int32 [batch + 1]: first new token of each request, then their number
+ *   slots        device int32 [max_tokens], 16-byte aligned: slot of each new token, -1
+ *                behind the last one (kvq_quantize skips those)
+ *   positions    device int32 [max_tokens], 16-byte aligned, or NULL: position of each new
+ *                token in its sequence, 0 behind the last one
+ *   workspace    device, >= 256 bytes, 16-byte aligned, initialized once with
+ *                kvq_workspace_init; only its flag word is used
+ * A step that cannot be done changes nothing but entries of free_pages above the count: it
+ * sets a flag (KVQ_FLAG_BAD_SEQLEN: n_b < 0, a_b < -1 or n_b + a_b > max_pages * page_size;
+ * KVQ_FLAG_BAD_PAGE: a page id outside [0, num_pages) among the pages that the step moves or
+ * continues, or a count that does not fit the pool; KVQ_FLAG_NO_PAGES; KVQ_FLAG_NO_SLOTS),
+ * returns seq_lens and the count as they were, zero offsets and -1 slots.
+ * Apart from the two pairs named above the buffers must not overlap.  batch == 0 is a no-op.
+ */
+int kvq_plan_step(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages,
+                  int32_t max_tokens, const int32_t* seq_lens, const int32_t* new_lens,
+                  int32_t* free_pages, const int32_t* free_count, int32_t* page_table,
+                  int32_t* seq_lens_out, int32_t* free_count_out, int32_t* token_offsets,
+                  int32_t* slots, int32_t* positions, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* Workspace bytes of kvq_prompt_attn / kvq_prefix_attn for a request; 0 for arguments that
+ * the call refuses. */
+size_t kvq_prompt_workspace_size(const kvq_cache_desc* desc, int32_t n_tokens, int32_t num_q_heads,
+                                 int32_t batch, int32_t max_seq_len);
+size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int32_t num_q_heads,
+                                 int32_t num_groups, int32_t max_prefix_len, int32_t max_seq_len);
+
+/*
+ * kvq_prompt_attn -- attention of each request's new tokens (a prompt, a chunk of one, proposed
+ * tokens to verify) over its positions in the cache, the new ones among them: write K and V
+ * of the new tokens first (kvq_quantize_kv).
+ *   (No passage: the pages' kernel has one query token.  Dense softmax attention; the skip
+ *   threshold is for kvq_decode_attn: over hundreds of query rows some row keeps nearly
+ *   every position.)
+ *   q            device fp16 [n_tokens][num_q_heads][head_dim], 16-byte aligned: the new tokens
+ *                of all requests, packed
+ *   token_offsets device int32 [batch + 1], not decreasing, in [0, n_tokens]: request b's
+ *                tokens are rows token_offsets[b] .. token_offsets[b+1] - 1, the last ones of
+ *                its sequence (n_b = their number, possibly 0).  Rows of q outside every
+ *                request are padding: not read, and their output rows are left as they were.
+ *   k_codes .. page_table, max_pages   as for kvq_decode_attn
+ *   seq_lens     device int32 [batch]: positions of each sequence, the new tokens included, in
+ *                [0, min(max_seq_len, max_pages*page_size)]
+ *   causal       1: token i of request b sees the positions 0 .. seq_lens[b] - n_b + i;
+ *                0: every position.  A token that sees none gets zeros.
+ *   sm_scale     score scale, finite, of any sign
+ *   workspace    device, kvq_prompt_workspace_size(...) bytes, 16-byte aligned, initialized
+ *                once with kvq_workspace_init; also used by kvq_prefix_attn calls if it is large
+ *                enough, but not by kvq_decode_attn
+ *   out          device [n_tokens][num_q_heads][head_dim] of out_type, 16-byte aligned
+ *   out_type     KVQ_OUT_F32 or KVQ_OUT_F16 (one rounding of the fp32 result)
+ * K and V values are rounded to fp16 once dequantized, the weights to fp16 for the product
+ * with V; scores, softmax statistics and sums are fp32.
+ * Same limits as kvq_decode_attn (KVQ_MAX_GROUP, KVQ_MAX_BATCH); max_seq_len <= 2^30.
+ * Sequences whose length, offsets or pages are out of range set KVQ_FLAG_BAD_SEQLEN /
+ * KVQ_FLAG_BAD_PAGE and nothing outside the buffers is touched.
+ */
+int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
+                    int32_t num_q_heads, const void* k_codes, const void* k_scales,
+                    const void* v_codes, const void* v_scales, const int32_t* page_table,
+                    int32_t max_pages, const int32_t* seq_lens, int32_t max_seq_len,
+                    const int32_t* token_offsets, int32_t batch, int32_t causal, float sm_scale,
+                    void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
+                    void* stream);
+
+/*
+ * kvq_prefix_attn -- single-token decode attention for requests that share long prefixes: a
+ * softmax over the positions of the request's group's prefix and its own, with each prefix read
+ * and scored once for all query rows of its group.
+ *   (No passage: the pages' kernel has one sequence.  Dense, as kvq_prompt_attn.)
+ *   q            device fp16 [batch][num_q_heads][head_dim], 16-byte aligned
+ *   prefix_table device int32 [num_groups][max_prefix_pages], or NULL: prefix g uses the pages
+ *                g*max_prefix_pages ..
+ *   prefix_lens  device int32 [num_groups], each in [0, min(max_prefix_len,
+ *                max_prefix_pages*page_size)]; any length, not only whole pages
+ *   group_offsets device int32 [num_groups + 1], not decreasing, in [0, batch]: group g is
+ *                the requests group_offsets[g] .. group_offsets[g+1] - 1; requests outside every
+ *                group have no prefix.  NULL: one group (num_groups = 1) of all requests.
+ *   page_table, max_pages, seq_lens, max_seq_len   the requests' own positions, as for
+ *                kvq_decode_attn (page_table NULL: pages b*max_pages ..); a length may be 0
+ *   other arguments as for kvq_prompt_attn; the workspace is kvq_prefix_workspace_size(...)
+ * A request without any position gets zeros.
+ */
+int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_t num_q_heads,
+                    const void* k_codes, const void* k_scales, const void* v_codes,
+                    const void* v_scales, const int32_t* prefix_table, int32_t max_prefix_pages,
+                    const int32_t* prefix_lens, int32_t max_prefix_len,
+                    const int32_t* group_offsets, int32_t num_groups, const int32_t* page_table,
+                    int32_t max_pages, const int32_t* seq_lens, int32_t max_seq_len, float sm_scale,
+                    void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
+                    void* stream);
 
 /*
  * kvq_lloyd_max_codebook -- the minimum-MSE `levels`-entry scalar codebook for

@@ -37,6 +37,11 @@ KVQ_OPT_V_WITH_K = 8
 KVQ_FLAG_BAD_PAGE = 1
 KVQ_FLAG_BAD_SEQLEN = 2
 KVQ_FLAG_TIMEOUT = 4
+KVQ_FLAG_NO_PAGES = 8
+KVQ_FLAG_NO_SLOTS = 16
+
+KVQ_OUT_F32 = 0
+KVQ_OUT_F16 = 1
 
 KVQ_MAX_GROUP = 8
 KVQ_MAX_SPLIT_TOKENS = 1024
@@ -89,6 +94,13 @@ def _load():
         "kvq_decode_attn_noalloc": (ctypes.c_int, [D, P, I32, I32, P, P, P, P, P, I32, P, I32, F32,
                                                    F32, I32, U32, P, P, P]),
         "kvq_noalloc_read_flags": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), P]),
+        "kvq_plan_step": (ctypes.c_int, [I32] * 5 + [P] * 11 + [SZ, P]),
+        "kvq_prompt_workspace_size": (SZ, [D, I32, I32, I32, I32]),
+        "kvq_prefix_workspace_size": (SZ, [D, I32, I32, I32, I32, I32]),
+        "kvq_prompt_attn": (ctypes.c_int, [D, P, I32, I32, P, P, P, P, P, I32, P, I32, P, I32, I32,
+                                           F32, P, SZ, P, I32, P]),
+        "kvq_prefix_attn": (ctypes.c_int, [D, P, I32, I32, P, P, P, P, P, I32, P, I32, P, I32, P,
+                                           I32, P, I32, F32, P, SZ, P, I32, P]),
         "kvq_lloyd_max_codebook": (ctypes.c_int, [I32, ctypes.c_double,
                                                   ctypes.POINTER(ctypes.c_uint16)]),
         "kvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -263,3 +275,59 @@ def kvq_noalloc_read_flags(stream=None) -> int:
     flags = ctypes.c_uint32(0)
     _check("kvq_noalloc_read_flags", _lib.kvq_noalloc_read_flags(ctypes.byref(flags), _stream(stream)))
     return int(flags.value)
+
+
+def kvq_plan_step(batch: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int,
+                  seq_lens, new_lens, free_pages, free_count, page_table, seq_lens_out,
+                  free_count_out, token_offsets, slots, positions, workspace, workspace_bytes: int,
+                  stream=None, check: bool = True) -> int:
+    st = _lib.kvq_plan_step(batch, page_size, num_pages, max_pages, max_tokens, _ptr(seq_lens),
+                            _ptr(new_lens), _ptr(free_pages), _ptr(free_count), _ptr(page_table),
+                            _ptr(seq_lens_out), _ptr(free_count_out), _ptr(token_offsets),
+                            _ptr(slots), _ptr(positions), _ptr(workspace), int(workspace_bytes),
+                            _stream(stream))
+    if check:
+        _check("kvq_plan_step", st)
+    return st
+
+
+def kvq_prompt_workspace_size(desc: KvqCacheDesc, n_tokens: int, num_q_heads: int, batch: int,
+                              max_seq_len: int) -> int:
+    return _lib.kvq_prompt_workspace_size(ctypes.byref(desc), n_tokens, num_q_heads, batch, max_seq_len)
+
+
+def kvq_prefix_workspace_size(desc: KvqCacheDesc, batch: int, num_q_heads: int, num_groups: int,
+                              max_prefix_len: int, max_seq_len: int) -> int:
+    return _lib.kvq_prefix_workspace_size(ctypes.byref(desc), batch, num_q_heads, num_groups,
+                                          max_prefix_len, max_seq_len)
+
+
+def kvq_prompt_attn(desc: KvqCacheDesc, q, n_tokens: int, num_q_heads: int, k_codes, k_scales,
+                    v_codes, v_scales, page_table, max_pages: int, seq_lens, max_seq_len: int,
+                    token_offsets, batch: int, causal: bool, sm_scale: float, workspace,
+                    workspace_bytes: int, out, out_type: int = KVQ_OUT_F32, stream=None,
+                    check: bool = True) -> int:
+    st = _lib.kvq_prompt_attn(ctypes.byref(desc), _ptr(q), n_tokens, num_q_heads, _ptr(k_codes),
+                              _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(page_table),
+                              max_pages, _ptr(seq_lens), max_seq_len, _ptr(token_offsets), batch,
+                              int(causal), float(sm_scale), _ptr(workspace), int(workspace_bytes),
+                              _ptr(out), int(out_type), _stream(stream))
+    if check:
+        _check("kvq_prompt_attn", st)
+    return st
+
+
+def kvq_prefix_attn(desc: KvqCacheDesc, q, batch: int, num_q_heads: int, k_codes, k_scales, v_codes,
+                    v_scales, prefix_table, max_prefix_pages: int, prefix_lens, max_prefix_len: int,
+                    group_offsets, num_groups: int, page_table, max_pages: int, seq_lens,
+                    max_seq_len: int, sm_scale: float, workspace, workspace_bytes: int, out,
+                    out_type: int = KVQ_OUT_F32, stream=None, check: bool = True) -> int:
+    st = _lib.kvq_prefix_attn(ctypes.byref(desc), _ptr(q), batch, num_q_heads, _ptr(k_codes),
+                              _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(prefix_table),
+                              max_prefix_pages, _ptr(prefix_lens), max_prefix_len,
+                              _ptr(group_offsets), num_groups, _ptr(page_table), max_pages,
+                              _ptr(seq_lens), max_seq_len, float(sm_scale), _ptr(workspace),
+                              int(workspace_bytes), _ptr(out), int(out_type), _stream(stream))
+    if check:
+        _check("kvq_prefix_attn", st)
+    return st

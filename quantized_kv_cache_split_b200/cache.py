@@ -54,6 +54,8 @@ class QuantizedKVCache:
         self.desc = kb.make_desc(fmt, head_dim, num_kv_heads, page_size, num_pages,
                                  self.codebook, self.signs)
         self._ws = None
+        self._ws_rows = None     # prompt and prefix attention
+        self._rows_bytes = {}    # workspace bytes by request shape
 
     # ---------------------------------------------------------------- writes
     def write(self, k: torch.Tensor, v: torch.Tensor, slots: Optional[torch.Tensor] = None,
@@ -110,5 +112,107 @@ class QuantizedKVCache:
             kb.kvq_combine(self.desc, ws, B, Hq, max_seq_len, L, seq_lens, out, opts, stream)
         return out
 
+    # ---------------------------------------------------------------- prompts, shared prefixes
+    def _rows_workspace(self, key, size_fn, args, stream):
+        nbytes = self._rows_bytes.get(key)
+        if nbytes is None:
+            nbytes = self._rows_bytes[key] = size_fn(self.desc, *args)
+        if self._ws_rows is None or self._ws_rows.numel() < nbytes:
+            self._ws_rows = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            kb.kvq_workspace_init(self._ws_rows, self._ws_rows.numel(), stream)
+        return self._ws_rows
+
+    def _rows_out(self, q, out, out_dtype):
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype, device=self.device)
+        return out, _OUT_TYPES[out.dtype]
+
+    def prompt_attention(self, q: torch.Tensor, token_offsets: torch.Tensor, seq_lens: torch.Tensor,
+                         max_seq_len: int, page_table: Optional[torch.Tensor] = None,
+                         max_pages: int = 1, causal: bool = True, sm_scale: Optional[float] = None,
+                         out: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+                         stream=None) -> torch.Tensor:
+        """Attention of each request's new tokens over its positions in the cache.
+
+        ``q`` [n_tokens, num_q_heads, head_dim] (fp16): the new tokens of all requests,
+        packed; request b's are rows ``token_offsets[b]`` .. ``token_offsets[b + 1] - 1``
+        and the last ones of its ``seq_lens[b]`` positions (write their K and V first).
+        ``causal``: a token sees the positions up to its own.  Rows outside every request are
+        padding and keep what ``out`` holds there."""
+        n, Hq, D = q.shape
+        B = seq_lens.shape[0]
+        ws = self._rows_workspace(("prompt", n, Hq, B, max_seq_len), kb.kvq_prompt_workspace_size,
+                                  (n, Hq, B, max_seq_len), stream)
+        out, kind = self._rows_out(q, out, out_dtype)
+        kb.kvq_prompt_attn(self.desc, q, n, Hq, self.k_codes, self.k_scales, self.v_codes,
+                           self.v_scales, page_table, max_pages, seq_lens, max_seq_len,
+                           token_offsets, B, causal, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale,
+                           ws, ws.numel(), out, kind, stream)
+        return out
+
+    def prefix_attention(self, q: torch.Tensor, prefix_table: Optional[torch.Tensor],
+                         prefix_lens: torch.Tensor, max_prefix_len: int, seq_lens: torch.Tensor,
+                         max_seq_len: int, page_table: Optional[torch.Tensor] = None,
+                         max_pages: int = 1, group_offsets: Optional[torch.Tensor] = None,
+                         max_prefix_pages: Optional[int] = None, sm_scale: Optional[float] = None,
+                         out: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+                         stream=None) -> torch.Tensor:
+        """Decode attention of q [batch, num_q_heads, head_dim] (fp16) for requests that share
+        prefixes: group g (requests ``group_offsets[g]`` .. ``group_offsets[g + 1] - 1``; None:
+        one group of all) attends to the ``prefix_lens[g]`` positions of row g of
+        ``prefix_table`` and each request to its own ``seq_lens[b]`` positions as well.  The
+        prefix is read once per group, not once per request."""
+        B, Hq, D = q.shape
+        ng = prefix_lens.shape[0]
+        if max_prefix_pages is None:
+            if prefix_table is None:
+                raise ValueError("max_prefix_pages is needed without a prefix_table")
+            max_prefix_pages = prefix_table.shape[1]
+        ws = self._rows_workspace(("prefix", B, Hq, ng, max_prefix_len, max_seq_len),
+                                  kb.kvq_prefix_workspace_size, (B, Hq, ng, max_prefix_len, max_seq_len),
+                                  stream)
+        out, kind = self._rows_out(q, out, out_dtype)
+        kb.kvq_prefix_attn(self.desc, q, B, Hq, self.k_codes, self.k_scales, self.v_codes,
+                           self.v_scales, prefix_table, max_prefix_pages, prefix_lens, max_prefix_len,
+                           group_offsets, ng, page_table, max_pages, seq_lens, max_seq_len,
+                           1.0 / math.sqrt(D) if sm_scale is None else sm_scale, ws, ws.numel(), out,
+                           kind, stream)
+        return out
+
     def device_flags(self) -> int:
-        return 0 if self._ws is None else kb.kvq_read_device_flags(self._ws)
+        flags = 0 if self._ws is None else kb.kvq_read_device_flags(self._ws)
+        return flags if self._ws_rows is None else flags | kb.kvq_read_device_flags(self._ws_rows)
+
+
+_OUT_TYPES = {torch.float32: kb.KVQ_OUT_F32, torch.float16: kb.KVQ_OUT_F16}
+
+
+class PagePlanner:
+    """The page bookkeeping of serving steps on the GPU (kvq_plan_step).
+
+    Owns the buffers a step writes: ``seq_lens`` [batch], ``token_offsets`` [batch + 1],
+    ``slots`` and ``positions`` [max_tokens], ``free_count`` [1].  The page table and the stack
+    of free pages are the caller's and are updated in place; pass ``planner.seq_lens`` and
+    ``planner.free_count`` back in for the next step to keep the whole state on the GPU."""
+
+    def __init__(self, batch: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int,
+                 device="cuda"):
+        self.batch, self.page_size, self.num_pages = batch, page_size, num_pages
+        self.max_pages, self.max_tokens = max_pages, max_tokens
+        self.device = torch.device(device)
+        ints = lambda n: torch.zeros(n, dtype=torch.int32, device=self.device)  # noqa: E731
+        self.seq_lens, self.token_offsets, self.free_count = ints(batch), ints(batch + 1), ints(1)
+        self.slots, self.positions = ints(max_tokens), ints(max_tokens)
+        self._ws = torch.zeros(256, dtype=torch.uint8, device=self.device)
+
+    def step(self, new_lens: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+             free_pages: torch.Tensor, free_count: torch.Tensor, stream=None) -> None:
+        """Plan one step: ``new_lens[b]`` tokens to append per request, -1 where it ends."""
+        kb.kvq_plan_step(self.batch, self.page_size, self.num_pages, self.max_pages, self.max_tokens,
+                         seq_lens, new_lens, free_pages, free_count, page_table, self.seq_lens,
+                         self.free_count, self.token_offsets, self.slots, self.positions, self._ws,
+                         256, stream)
+
+    def device_flags(self) -> int:
+        """KVQ_FLAG_* bits of the steps so far (a flagged step changed nothing)."""
+        return kb.kvq_read_device_flags(self._ws)

@@ -33,10 +33,6 @@ int device_sm_count() {
   return cache[dev];
 }
 
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 int check_desc(const kvq_cache_desc* d) {
   if (!d) return KVQ_ERR_INVALID_ARG;
   if (d->fmt != KVQ_FMT_Q8_0 && d->fmt != KVQ_FMT_Q4_0 && d->fmt != KVQ_FMT_LUT4 &&
@@ -51,6 +47,8 @@ int check_desc(const kvq_cache_desc* d) {
   if (d->fmt == KVQ_FMT_LUT4 && (reinterpret_cast<uintptr_t>(d->signs) & 7u)) return KVQ_ERR_INVALID_ARG;
   return KVQ_OK;
 }
+
+namespace {
 
 int max_splits_for(int max_seq_len, int split_tokens) {
   return (max_seq_len + split_tokens - 1) / split_tokens;

@@ -76,4 +76,8 @@ int launch_combine(const kvq_cache_desc& desc, const void* workspace, int batch,
 
 int device_sm_count();
 
+// KVQ_OK if the library can serve this cache, else why not (kvq_api.cu).
+int check_desc(const kvq_cache_desc* d);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 }  // namespace kvq

@@ -44,6 +44,7 @@ quant_q8_0_kernel(const __half* __restrict__ x, const __half* __restrict__ x2, i
   const int64_t tok = vec / hkv;
   const int h = (int)(vec - tok * hkv);
   const int64_t slot = slots ? (int64_t)slots[tok] : tok;
+  if (slot < 0) return;  // a padding token (warp-uniform)
   const int64_t row = slot_row(slot, page_size, hkv, h);
   const __half* xv = x + vec * D;
   float d_mine = 0.f;
@@ -82,6 +83,7 @@ quant_q4_0_kernel(const __half* __restrict__ x, const __half* __restrict__ x2, i
   const int64_t tok = vec / hkv;
   const int h = (int)(vec - tok * hkv);
   const int64_t slot = slots ? (int64_t)slots[tok] : tok;
+  if (slot < 0) return;  // a padding token (warp-uniform)
   const int64_t row = slot_row(slot, page_size, hkv, h);
   const __half* xv = x + vec * D;
   float d_mine = 0.f;
@@ -139,6 +141,7 @@ quant_lut4_kernel(const __half* __restrict__ x, const __half* __restrict__ x2, i
   const int64_t tok = vec / hkv;
   const int h = (int)(vec - tok * hkv);
   const int64_t slot = slots ? (int64_t)slots[tok] : tok;
+  if (slot < 0) return;  // a padding token (warp-uniform)
   const int64_t row = slot_row(slot, page_size, hkv, h);
   const __half* xv = x + vec * D;
 
@@ -267,6 +270,7 @@ quant_nvfp4_kernel(const __half* __restrict__ x, const __half* __restrict__ x2, 
   const int64_t tok = vec / hkv;
   const int h = (int)(vec - tok * hkv);
   const int64_t slot = slots ? (int64_t)slots[tok] : tok;
+  if (slot < 0) return;  // a padding token (warp-uniform)
   const int64_t row = slot_row(slot, page_size, hkv, h);
   const __half* xv = x + vec * D;
   float v[NM];

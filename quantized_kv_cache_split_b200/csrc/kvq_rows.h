@@ -1,0 +1,73 @@
+// Internal interface of the many-row attention kernel (kvq_rows.cu) and the merge of its
+// partials (kvq_rows_merge.cu).
+#pragma once
+
+#include "kvq_internal.h"
+
+namespace kvq {
+
+constexpr int kRowTile = 256;   // query rows of one unit (two TMEM row tiles of 128)
+constexpr int kKvTile = 128;    // positions of one K / V tile
+constexpr int kTargetCtas = 148;  // SMs of a B200: one CTA each
+
+// Attention of many query rows over groups of positions.  Group g owns the tokens
+// offsets[g] .. offsets[g + 1] - 1 (a row is one query head of one token; the heads of one
+// KV head are consecutive rows) and the positions 0 .. lens[g] - 1 of its pages.
+struct RowsArgs {
+  kvq_cache_desc desc;
+  const void* q;           // fp16 [n_tokens][num_q_heads][head_dim]
+  int n_tokens, num_q_heads, group;
+  const void* k_codes;
+  const void* k_scales;
+  const void* v_codes;
+  const void* v_scales;
+  const int32_t* table;    // [num_groups][max_pages], or null: pages g*max_pages ..
+  int max_pages;
+  const int32_t* lens;     // [num_groups]
+  int max_len;
+  const int32_t* offsets;  // [num_groups + 1], or null: one group of every token
+  int num_groups;
+  int causal;              // token i of n sees the positions < lens - n + i + 1; else all
+  float sm_scale;
+  int splits, chunk;       // each unit's positions are cut at multiples of chunk (of kKvTile)
+  int row_tiles;           // row tiles of all groups at the most
+  // out != null: one split, the rows are normalized and written here; otherwise partials:
+  float* part_o;           // [n_tokens][num_q_heads][splits][head_dim], unnormalized
+  float* part_m;           // [n_tokens][num_q_heads][splits] running maximum, log2 units
+  float* part_l;           // [n_tokens][num_q_heads][splits]
+  void* out;
+  int out_f16;
+  uint32_t* flags;
+};
+
+// The split of a request: row tiles, splits and positions per split.
+struct RowsPlan {
+  int row_tiles, splits, chunk;
+};
+RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, int max_len);
+size_t rows_partial_bytes(int n_tokens, int num_q_heads, int head_dim, int splits);
+
+int launch_rows(const RowsArgs& a, cudaStream_t stream);
+
+// Merge of the partials of a rows launch and, when seq_lens is given, of a decode launch
+// (one token per request, same rows) into the normalized output; lut4 is rotated back.
+struct MergeArgs {
+  RowsArgs rows;
+  const int32_t* seq_lens;  // own positions of each token's request, or null
+  int max_seq_len, split_tokens, max_splits;
+  const float* own_o;       // [n_tokens][num_q_heads][max_splits][head_dim]
+  const float* own_m;
+  const float* own_l;
+  void* out;
+  int out_f16;
+};
+int launch_rows_merge(const MergeArgs& a, cudaStream_t stream);
+
+// The visible positions of token i of a group of n tokens and `len` positions.
+__host__ __device__ inline int row_limit(int len, int n, int i, int causal) {
+  if (!causal) return len;
+  const int lim = len - n + i + 1;
+  return lim < 0 ? 0 : lim;
+}
+
+}  // namespace kvq

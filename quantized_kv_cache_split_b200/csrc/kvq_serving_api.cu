@@ -1,0 +1,246 @@
+// C-ABI entry points of the serving operators: the page plan of a step, prompt attention and
+// shared-prefix decode.  Argument validation, then the launches; nothing is launched on an error.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kvq_device.cuh"
+#include "kvq_plan.h"
+#include "kvq_rows.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kMaxLen = 1 << 30;
+
+// What kvq_prompt_attn and kvq_prefix_attn ask of a request besides its pointers.
+int check_rows(const kvq_cache_desc* desc, int64_t n_tokens, int num_q_heads, int groups, int max_len) {
+  const int st = check_desc(desc);
+  if (st != KVQ_OK) return st;
+  if (n_tokens < 0 || num_q_heads < 1 || groups < 0 || max_len < 0) return KVQ_ERR_INVALID_ARG;
+  if (num_q_heads % desc->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
+  if (num_q_heads / desc->num_kv_heads > KVQ_MAX_GROUP || groups > KVQ_MAX_BATCH || max_len > kMaxLen)
+    return KVQ_ERR_UNSUPPORTED;
+  if (n_tokens * num_q_heads > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+// lut4 rows are rotated back by the merge kernel, so they always go through it.
+bool needs_merge(const kvq_cache_desc* desc, const RowsPlan& p) {
+  return p.splits > 1 || desc->fmt == KVQ_FMT_LUT4;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Positions per split of the requests' own part of prefix decode: about one split per CTA
+// slot (four CTAs of four warps per SM), 128 to 512 positions.
+int own_split(const kvq_cache_desc* desc, int batch, int max_seq_len) {
+  const int64_t pairs = (int64_t)std::max(batch, 1) * desc->num_kv_heads;
+  const int64_t l = (pairs * max_seq_len + 4 * kTargetCtas - 1) / (4 * kTargetCtas);
+  return (int)std::min<int64_t>(std::max<int64_t>((l + kTile - 1) / kTile * kTile, 128), 512);
+}
+
+// Pointers into a rows workspace at `at`.
+void set_partials(RowsArgs* r, uint8_t* at) {
+  const size_t n = (size_t)r->n_tokens * r->num_q_heads * r->splits;
+  r->part_o = reinterpret_cast<float*>(at);
+  r->part_m = r->part_o + n * r->desc.head_dim;
+  r->part_l = r->part_m + n;
+}
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" {
+
+int kvq_plan_step(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages,
+                  int32_t max_tokens, const int32_t* seq_lens, const int32_t* new_lens,
+                  int32_t* free_pages, const int32_t* free_count, int32_t* page_table,
+                  int32_t* seq_lens_out, int32_t* free_count_out, int32_t* token_offsets,
+                  int32_t* slots, int32_t* positions, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  if (batch < 0 || num_pages < 1 || max_pages < 1 || max_tokens < 0) return KVQ_ERR_INVALID_ARG;
+  if (page_size < 64 || page_size % 64 != 0) return KVQ_ERR_UNSUPPORTED;
+  if (batch > KVQ_MAX_BATCH || (int64_t)num_pages * page_size > 0x7fffffffLL ||
+      (int64_t)max_pages * page_size > 0x7fffffffLL)
+    return KVQ_ERR_UNSUPPORTED;
+  if (!seq_lens || !new_lens || !free_pages || !free_count || !page_table || !seq_lens_out || !free_count_out ||
+      !token_offsets || (!slots && max_tokens > 0) || !workspace)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(slots) || !aligned16(positions) || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  if (workspace_bytes < kWorkspaceHeader) return KVQ_ERR_WORKSPACE;
+  if (batch == 0) return KVQ_OK;
+  PlanArgs a;
+  a.batch = batch;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.max_tokens = max_tokens;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.page_table = page_table;
+  a.seq_lens_out = seq_lens_out;
+  a.free_count_out = free_count_out;
+  a.token_offsets = token_offsets;
+  a.slots = slots;
+  a.positions = positions;
+  a.flags = static_cast<uint32_t*>(workspace);
+  return launch_plan(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t kvq_prompt_workspace_size(const kvq_cache_desc* desc, int32_t n_tokens, int32_t num_q_heads,
+                                 int32_t batch, int32_t max_seq_len) {
+  if (check_rows(desc, n_tokens, num_q_heads, batch, max_seq_len) != KVQ_OK) return 0;
+  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len);
+  return kWorkspaceHeader +
+         (needs_merge(desc, p) ? rows_partial_bytes(n_tokens, num_q_heads, desc->head_dim, p.splits) : 0);
+}
+
+size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int32_t num_q_heads,
+                                 int32_t num_groups, int32_t max_prefix_len, int32_t max_seq_len) {
+  if (check_rows(desc, batch, num_q_heads, num_groups, max_prefix_len) != KVQ_OK) return 0;
+  if (batch > KVQ_MAX_BATCH || max_seq_len < 0 || max_seq_len > kMaxLen) return 0;
+  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, batch, num_groups, max_prefix_len);
+  return round256(kvq_workspace_size(batch, num_q_heads, desc->head_dim, max_seq_len,
+                                     own_split(desc, batch, max_seq_len))) +
+         rows_partial_bytes(batch, num_q_heads, desc->head_dim, p.splits);
+}
+
+int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
+                    int32_t num_q_heads, const void* k_codes, const void* k_scales,
+                    const void* v_codes, const void* v_scales, const int32_t* page_table,
+                    int32_t max_pages, const int32_t* seq_lens, int32_t max_seq_len,
+                    const int32_t* token_offsets, int32_t batch, int32_t causal, float sm_scale,
+                    void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
+                    void* stream) {
+  int st = check_rows(desc, n_tokens, num_q_heads, batch, max_seq_len);
+  if (st != KVQ_OK) return st;
+  if (max_pages < 1 || (causal != 0 && causal != 1) || (out_type != KVQ_OUT_F32 && out_type != KVQ_OUT_F16) ||
+      !isfinite(sm_scale))
+    return KVQ_ERR_INVALID_ARG;
+  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !seq_lens || !token_offsets || !workspace || !out)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
+      !aligned16(workspace) || !aligned16(out))
+    return KVQ_ERR_INVALID_ARG;
+  if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
+  if (workspace_bytes < kvq_prompt_workspace_size(desc, n_tokens, num_q_heads, batch, max_seq_len))
+    return KVQ_ERR_WORKSPACE;
+  if (batch == 0 || n_tokens == 0) return KVQ_OK;
+  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len);
+  const bool merge = needs_merge(desc, p);
+  MergeArgs m{};
+  RowsArgs& r = m.rows;
+  r.desc = *desc;
+  r.q = q;
+  r.n_tokens = n_tokens;
+  r.num_q_heads = num_q_heads;
+  r.group = num_q_heads / desc->num_kv_heads;
+  r.k_codes = k_codes;
+  r.k_scales = k_scales;
+  r.v_codes = v_codes;
+  r.v_scales = v_scales;
+  r.table = page_table;
+  r.max_pages = max_pages;
+  r.lens = seq_lens;
+  r.max_len = max_seq_len;
+  r.offsets = token_offsets;
+  r.num_groups = batch;
+  r.causal = causal;
+  r.sm_scale = sm_scale;
+  r.splits = p.splits;
+  r.chunk = p.chunk;
+  r.row_tiles = p.row_tiles;
+  r.flags = static_cast<uint32_t*>(workspace);
+  if (merge) set_partials(&r, static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
+  else r.out = out;
+  r.out_f16 = out_type == KVQ_OUT_F16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = launch_rows(r, s);
+  if (st != KVQ_OK || !merge) return st;
+  m.out = out;
+  m.out_f16 = r.out_f16;
+  return launch_rows_merge(m, s);
+}
+
+int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_t num_q_heads,
+                    const void* k_codes, const void* k_scales, const void* v_codes,
+                    const void* v_scales, const int32_t* prefix_table, int32_t max_prefix_pages,
+                    const int32_t* prefix_lens, int32_t max_prefix_len,
+                    const int32_t* group_offsets, int32_t num_groups, const int32_t* page_table,
+                    int32_t max_pages, const int32_t* seq_lens, int32_t max_seq_len, float sm_scale,
+                    void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
+                    void* stream) {
+  int st = check_rows(desc, batch, num_q_heads, num_groups, max_prefix_len);
+  if (st != KVQ_OK) return st;
+  if (max_prefix_pages < 1 || max_pages < 1 || max_seq_len < 0 || num_groups < 1 ||
+      (out_type != KVQ_OUT_F32 && out_type != KVQ_OUT_F16) || !isfinite(sm_scale))
+    return KVQ_ERR_INVALID_ARG;
+  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !prefix_lens || !seq_lens || !workspace || !out)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
+      !aligned16(workspace) || !aligned16(out))
+    return KVQ_ERR_INVALID_ARG;
+  if (!group_offsets && num_groups != 1) return KVQ_ERR_INVALID_ARG;
+  if (!prefix_table && (int64_t)num_groups * max_prefix_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
+  if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
+  const int L = own_split(desc, batch, max_seq_len);
+  const int max_splits = (max_seq_len + L - 1) / L;
+  if (batch > KVQ_MAX_BATCH || max_seq_len > kMaxLen || max_splits > KVQ_MAX_SPLITS) return KVQ_ERR_UNSUPPORTED;
+  if (workspace_bytes < kvq_prefix_workspace_size(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len))
+    return KVQ_ERR_WORKSPACE;
+  if (batch == 0) return KVQ_OK;
+  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, batch, num_groups, max_prefix_len);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t own_bytes = kvq_workspace_size(batch, num_q_heads, desc->head_dim, max_seq_len, L);
+  MergeArgs m{};
+  RowsArgs& r = m.rows;
+  r.desc = *desc;
+  r.q = q;
+  r.n_tokens = batch;
+  r.num_q_heads = num_q_heads;
+  r.group = num_q_heads / desc->num_kv_heads;
+  r.k_codes = k_codes;
+  r.k_scales = k_scales;
+  r.v_codes = v_codes;
+  r.v_scales = v_scales;
+  r.table = prefix_table;
+  r.max_pages = max_prefix_pages;
+  r.lens = prefix_lens;
+  r.max_len = max_prefix_len;
+  r.offsets = group_offsets;
+  r.num_groups = num_groups;
+  r.causal = 0;
+  r.sm_scale = sm_scale;
+  r.splits = p.splits;
+  r.chunk = p.chunk;
+  r.row_tiles = p.row_tiles;
+  r.flags = reinterpret_cast<uint32_t*>(ws);
+  set_partials(&r, ws + round256(own_bytes));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // the requests' own positions: the decode kernel, its partials left in the workspace
+  st = kvq_decode_attn(desc, q, batch, num_q_heads, k_codes, k_scales, v_codes, v_scales, page_table, max_pages,
+                       seq_lens, max_seq_len, sm_scale, 0.f, L, 0u, workspace, own_bytes, nullptr, nullptr, stream);
+  if (st != KVQ_OK) return st;
+  if (max_prefix_len > 0) {
+    st = launch_rows(r, s);
+    if (st != KVQ_OK) return st;
+  }
+  m.seq_lens = seq_lens;
+  m.max_seq_len = max_seq_len;
+  m.split_tokens = L;
+  m.max_splits = max_splits;
+  const size_t n_own = (size_t)batch * num_q_heads * max_splits;
+  m.own_o = reinterpret_cast<const float*>(ws + kWorkspaceHeader + counters_bytes(batch, num_q_heads) + 16 * n_own);
+  m.own_m = m.own_o + n_own * desc->head_dim;
+  m.own_l = m.own_m + n_own;
+  m.out = out;
+  m.out_f16 = out_type == KVQ_OUT_F16;
+  return launch_rows_merge(m, s);
+}
+
+}  // extern "C"
