@@ -5,16 +5,18 @@
 //   S = Q K^T,  P = 2^(S sm_scale log2(e) - m),  O = P V,  l = sum P
 //
 // with the running maximum m of a streaming softmax, one pass over the positions.  Both
-// products run on the fifth-generation tensor cores.  One CTA (17 warps) per unit:
+// products run on the fifth-generation tensor cores.  One CTA per unit:
 // (group, KV head, 256 query rows, split of the positions).
 //
 //   warps 0-3, 4-7   softmax of row tile 0 / 1 (stream 0 / 1): one thread per row.  Scores
 //                    come from TMEM, weights go back to TMEM as fp16 (the A operand of P V)
 //                    over the scores.  The accumulator is rescaled only when the maximum
 //                    has grown by more than 2^8: until then the weights stay below 2^15.
-//   warps 8-15       dequantize: codes and scales of a 128-position K or V tile from global
-//                    memory to registers, one tile ahead, then as fp16 to shared memory.
+//   warps 8-15       dequantize K and V tiles of 128 positions to fp16 in shared memory, four
+//                    warps per half tile.
 //   warp 16          issues the MMAs.
+//   warp 17          copies the codes and scales of half tiles (64 positions: one contiguous
+//                    range of a page) into a ring of staging buffers, ahead of the dequantizers.
 //
 // A unit of more than 128 rows runs its two row tiles against the same K / V tiles, so a
 // tile is dequantized once for 256 rows.  A unit of at most 128 rows gives both streams
@@ -36,34 +38,51 @@ namespace kvq {
 namespace {
 
 constexpr int kSoftmaxWarps = 8, kFillWarps = 8;
-constexpr int kMmaWarp = kSoftmaxWarps + kFillWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kFillThreads = 32 * kFillWarps;
+constexpr int kMmaWarp = kSoftmaxWarps + kFillWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // a whole warpgroup for the MMA warp
+// Registers per thread by role, out of 96 x 640 at launch
+constexpr int kSoftmaxRegs = 168, kFillRegs = 56, kMmaRegs = 32;
+static_assert(256 * kSoftmaxRegs + 256 * kFillRegs + 128 * kMmaRegs <= 96 * kThreads, "register pool");
 constexpr float kWeightBits = 7.f;   // weights are 2^(s - m + 7)
 constexpr float kRescaleBits = 8.f;  // growth of the maximum before the accumulator is rescaled
+#ifndef POLY
+#define POLY 0
+#endif
+constexpr int kPolyPairs = POLY;        // of 8 pairs of weights, those computed on the FMA pipe
 constexpr uint32_t kTmemColumns = 512;
 // q8_0 and nvfp4 values enter the products halved (their rounded code * scale can pass the
 // largest fp16 value by a step); the factor goes into the score scale and the output.
 template <int FMT>
 constexpr float kUnhalve = FMT == KVQ_FMT_Q8_0 || FMT == KVQ_FMT_NVFP4 ? 2.f : 1.f;
 
+constexpr int kMaxRaw = 8;
 struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // K / V tile slots
-  uint64_t s_full[2], p_full[2];                          // scores / weights of a stream
+  uint64_t s_full[2], p_half[2], p_full[2];  // a stream's scores; first half, rest of its weights
+  uint64_t q_full;                                        // query rows
   uint64_t done;                                          // every MMA completed
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];         // staged codes and scales of half tiles
   uint32_t tmem;
   int unit[6];  // group, first token row, rows, positions, new tokens, valid
   float merge_m[128], merge_l[128];
 };
 
-template <int D>
+template <int FMT, int D>
 struct Smem {
+  using C = Cfg<FMT, D>;
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows of D fp16
   static constexpr int kQ = 0;                    // two row tiles
   static constexpr int kK = 2 * kTileBytes;       // two slots
   static constexpr int kV = 4 * kTileBytes;       // two slots
-  static constexpr int kBars = 6 * kTileBytes;
+  static constexpr int kRaw = 6 * kTileBytes;     // staged half tiles: 64 code rows, 64 scale rows
+  static constexpr int kRawCodes = kTile * C::CROW, kRawScales = kTile * C::SROW;
+  static constexpr int kRawBytes = kRawCodes + kRawScales;
+  static constexpr int kRoom = 227 * 1024 - 1024 - (int)sizeof(Shared) - kRaw;
+  static constexpr int kStages = kRoom / kRawBytes < kMaxRaw ? kRoom / kRawBytes : kMaxRaw;
+  static constexpr int kBars = kRaw + kStages * kRawBytes;
   static constexpr int kBytes = kBars + (int)sizeof(Shared) + 1024;  // slack: 1024-byte alignment
+  static_assert(256 * (D * 4 + 16) <= kRaw && 128 * (D * 4 + 16) <= kV, "room for the results");
+  static_assert(kStages >= 3 && kBars % 16 == 0 && kRawCodes % 128 == 0 && kRawScales % 16 == 0, "staging");
 };
 
 // Byte offset of 16-byte chunk c of a row in a [128][D] fp16 tile: column groups of 64, 128-byte
@@ -73,17 +92,6 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int c) {
 }
 
 // ------------------------------------------------------------------ dequantization
-template <int FMT, int D>
-struct Fill {
-  using C = Cfg<FMT, D>;
-  static constexpr int kChunks = C::CROW / 16;               // 16-byte code chunks of a row
-  static constexpr int kTasks = 128 * kChunks / kFillThreads;  // chunks per thread and tile
-  static_assert(kTasks >= 1, "a chunk for every thread");
-  uint4 code[kTasks];
-  uint32_t scale[kTasks];  // fp16 scale, or nvfp4: two E4M3 bytes
-  float vec[C::kNv ? kTasks : 1];
-};
-
 template <int FMT, int D>
 __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, __half2 d, const Lut& lut) {
   using C = Cfg<FMT, D>;
@@ -115,74 +123,52 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, __half2 d, c
   return r;
 }
 
-// This thread's codes and scales of a tile; rows at or past n_valid are zero.  base0 / base1:
-// cache rows of the tile's two 64-position halves (negative: nothing to read).
+// Dequantize a staged half tile (64 rows, those at or past n_valid as zeros) into rows row0 ..
+// row0 + 63 of a fp16 tile; 128 threads, 16 code bytes at a time.
 template <int FMT, int D>
-__device__ __forceinline__ void fill_load(Fill<FMT, D>& f, const uint8_t* __restrict__ codes,
-                                          const uint8_t* __restrict__ scales, int64_t base0, int64_t base1,
-                                          int n_valid, int tid) {
+__device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8_t* tile, int row0, int n_valid,
+                                          int tid, const Lut& lut) {
   using C = Cfg<FMT, D>;
-  using F = Fill<FMT, D>;
+  constexpr int kChunks = C::CROW / 16;          // 16-byte code chunks of a row
+  constexpr int kTasks = kTile * kChunks / 128;  // per thread
+  static_assert(kTasks >= 1, "a chunk for every thread");
+  const uint8_t* scales = raw + kTile * C::CROW;
 #pragma unroll
-  for (int i = 0; i < F::kTasks; ++i) {
-    const int task = i * kFillThreads + tid;
-    const int row = task / F::kChunks, j = task % F::kChunks;
-    const int64_t base = row < 64 ? base0 : base1;
-    f.code[i] = make_uint4(0u, 0u, 0u, 0u);
-    f.scale[i] = 0u;
-    if constexpr (C::kNv) f.vec[i] = 0.f;
-    if (row < n_valid && base >= 0) {
-      const int64_t at = base + (row & 63);
-      f.code[i] = __ldg(reinterpret_cast<const uint4*>(codes + at * C::CROW) + j);
-      const uint8_t* s = scales + at * C::SROW;
-      if constexpr (C::kQ8) {
-        f.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s) + (j >> 1));
-      } else if constexpr (C::kQ4) {
-        f.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s) + j);
-      } else if constexpr (C::kLut) {
-        f.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s));
-      } else {
-        f.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s) + j);
-        f.vec[i] = __ldg(reinterpret_cast<const float*>(s + D / 16));
-      }
-    }
-  }
-}
-
-template <int FMT, int D>
-__device__ __forceinline__ void fill_store(const Fill<FMT, D>& f, uint8_t* tile, int tid, const Lut& lut) {
-  using C = Cfg<FMT, D>;
-  using F = Fill<FMT, D>;
-#pragma unroll
-  for (int i = 0; i < F::kTasks; ++i) {
-    const int task = i * kFillThreads + tid;
-    const int row = task / F::kChunks, j = task % F::kChunks;
-    const uint32_t w[4] = {f.code[i].x, f.code[i].y, f.code[i].z, f.code[i].w};
-    // The threads of a row that write the second column group take their chunks in another
-    // order, so that eight neighbours write eight different bank groups.
-    if constexpr (C::kQ8) {
-      const __half2 d = __half2half2(__ushort_as_half((unsigned short)f.scale[i]));
-      const bool flip = (j >> 2) & 1;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint4 v = dequant8<FMT, D>(flip ? w[2 - 2 * c] : w[2 * c], flip ? w[3 - 2 * c] : w[2 * c + 1], d, lut);
-        *reinterpret_cast<uint4*>(tile + tile_offset(row, 2 * j + (c ^ (int)flip))) = v;
-      }
+  for (int i = 0; i < kTasks; ++i) {
+    // Row and code chunk: dealt so that eight neighbours read eight different bank groups of
+    // the staged codes and write eight different ones of the swizzled tile (whose two column
+    // groups coincide modulo the banks): rows next to each other take opposite row halves.
+    int row, j;
+    if constexpr (kChunks == 8) {
+      row = 2 * (tid >> 3) + (tid >> 2 & 1) + 32 * (i >> 1);
+      j = (tid & 3) + 4 * ((tid >> 2 & 1) ^ (i & 1));
+    } else if constexpr (kChunks == 4 && !C::kQ8) {
+      row = tid >> 1;
+      j = (tid & 1) + 2 * ((tid >> 2 & 1) ^ i);
     } else {
-      const bool flip = (j >> 1) & 1;
-      __half2 d0, d1;
-      if constexpr (C::kNv) {
-        d0 = __float2half2_rn(e4m3_float(f.scale[i] & 0xffu) * f.vec[i]);
-        d1 = __float2half2_rn(e4m3_float(f.scale[i] >> 8) * f.vec[i]);
-      } else {
-        d0 = d1 = __half2half2(__ushort_as_half((unsigned short)f.scale[i]));
-      }
+      row = (i * 128 + tid) / kChunks;
+      j = tid % kChunks;
+    }
+    uint4 u = *reinterpret_cast<const uint4*>(raw + row * C::CROW + j * 16);
+    const bool live = row < n_valid;
+    const uint8_t* sp = scales + row * C::SROW;
+    __half2 d0, d1;
+    if constexpr (C::kNv) {
+      const uint32_t e = lds16(sp + 2 * j);
+      const float g = *reinterpret_cast<const float*>(sp + D / 16);
+      d0 = __float2half2_rn(live ? e4m3_float(e & 0xffu) * g : 0.f);
+      d1 = __float2half2_rn(live ? e4m3_float(e >> 8) * g : 0.f);
+    } else {
+      const uint32_t b = lds16(sp + (C::kQ8 ? j >> 1 : C::kQ4 ? j : 0) * 2);
+      d0 = d1 = __half2half2(__ushort_as_half((unsigned short)(live ? b : 0u)));
+    }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    constexpr int kOut = C::kQ8 ? 2 : 4;  // 16-byte chunks of eight values
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool second = flip ? (c < 2) : (c >= 2);  // chunk c ^ 2 flip is in the second half
-        const uint4 v = dequant8<FMT, D>(flip ? w[c ^ 2] : w[c], 0u, second ? d1 : d0, lut);
-        *reinterpret_cast<uint4*>(tile + tile_offset(row, 4 * j + (flip ? c ^ 2 : c))) = v;
-      }
+    for (int c = 0; c < kOut; ++c) {
+      const uint4 v = C::kQ8 ? dequant8<FMT, D>(w[2 * c & 3], w[(2 * c + 1) & 3], d0, lut)
+                             : dequant8<FMT, D>(w[c], 0u, c < 2 ? d0 : d1, lut);
+      *reinterpret_cast<uint4*>(tile + tile_offset(row0 + row, kOut * j + c)) = v;
     }
   }
 }
@@ -248,7 +234,7 @@ __device__ __forceinline__ void find_unit(const RowsArgs& a, int t, int lane, in
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
   using C = Cfg<FMT, D>;
-  using S = Smem<D>;
+  using S = Smem<FMT, D>;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   Shared& sh = *reinterpret_cast<Shared*>(smem + S::kBars);
@@ -269,13 +255,21 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
         bar_init(&sh.k_empty[i], 1);
         bar_init(&sh.v_empty[i], 1);
         bar_init(&sh.s_full[i], 1);
+        bar_init(&sh.p_half[i], kSoftmaxWarps / 2);
         bar_init(&sh.p_full[i], kSoftmaxWarps / 2);
       }
+      bar_init(&sh.q_full, kSoftmaxWarps);
       bar_init(&sh.done, 1);
+      for (int i = 0; i < S::kStages; ++i) {
+        bar_init(&sh.raw_full[i], 1);
+        bar_init(&sh.raw_empty[i], kFillWarps / 2);
+      }
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   const int g = sh.unit[0], row0 = sh.unit[1], rows = sh.unit[2], len = sh.unit[3], tok0 = sh.unit[4], n = sh.unit[5];
   // positions of this split that any row of the unit sees
   const int last = n > 0 ? row_limit(len, n, (row0 + rows - 1) / G, a.causal) : 0;
@@ -285,109 +279,74 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
   const bool shared_tiles = rows > 128;  // both streams take every tile; else every other one
   const bool live = n > 0 && (tiles > 0 || a.out != nullptr);
 
-  // query rows, fp16, K-major, 128-byte swizzle; rows past the unit's are zero
-  if (live && tiles > 0) {
-    const __half* q = static_cast<const __half*>(a.q);
-    const bool zero = a.sm_scale == 0.f;
-    const uint32_t flip = a.sm_scale < 0.f ? 0x80008000u : 0u;  // the scale's sign goes into the query
-    if constexpr (!C::kLut) {
-      constexpr int kC = D / 8;
-      for (int i = tid; i < kRowTile * kC; i += kThreads) {
-        const int r = i / kC, c = i % kC;
-        const int rr = shared_tiles ? r : r & 127;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < rows && !zero) {
-          const int t = (row0 + rr) / G, h = (row0 + rr) % G;
-          v = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)(tok0 + t) * a.num_q_heads + kvh * G + h) * D) + c);
-          v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-        }
-        *reinterpret_cast<uint4*>(smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, c)) = v;
-      }
-    } else {
-      // rotated: (1/sqrt(D)) H (signs .* q); a warp per row, lane l holds E consecutive elements
-      constexpr int E = D / 32;
-      for (int r = warp; r < kRowTile; r += kThreads / 32) {
-        const int rr = shared_tiles ? r : r & 127;
-        float y[E];
-#pragma unroll
-        for (int k = 0; k < E; ++k) y[k] = 0.f;
-        if (rr < rows && !zero) {
-          const int t = (row0 + rr) / G, h = (row0 + rr) % G;
-          const __half* src = q + ((int64_t)(tok0 + t) * a.num_q_heads + kvh * G + h) * D + lane * E;
-#pragma unroll
-          for (int k = 0; k < E; ++k) y[k] = __half2float(src[k]) * (float)a.desc.signs[lane * E + k];
-        }
-#pragma unroll
-        for (int h = 1; h < E; h <<= 1)
-#pragma unroll
-          for (int k = 0; k < E; ++k)
-            if (!(k & h)) {
-              const float u = y[k], v = y[k + h];
-              y[k] = u + v;
-              y[k + h] = u - v;
-            }
-#pragma unroll
-        for (int b = 1; b < 32; b <<= 1)
-#pragma unroll
-          for (int k = 0; k < E; ++k) {
-            const float o = __shfl_xor_sync(0xffffffffu, y[k], b);
-            y[k] = (lane & b) ? o - y[k] : y[k] + o;
-          }
-        const float cs = D == 64 ? 0.125f : 0.08838834764831845f;  // 1/sqrt(D)
-        uint8_t* dst = smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, lane * E / 8) + (lane * E % 8) * 2;
-#pragma unroll
-        for (int k = 0; k < E; k += 2)
-          *reinterpret_cast<uint32_t*>(dst + 2 * k) = pack_h2(y[k] * cs, y[k + 1] * cs) ^ flip;
-      }
-    }
-    fence_async_shared();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = sh.tmem;
   bool ok = true;
 
   if (live && tiles > 0) {
-    if (warp == kMmaWarp) {
+    if (warp >= kMmaWarp) {
       // ---------------------------------------------------------------- MMA
-      if (lane == 0) {
+      regs_shrink<kMmaRegs>();
+      if (warp == kMmaWarp) {
+        // the whole warp walks the loop (so that addresses stay warp-uniform); one elected
+        // thread issues
         constexpr uint32_t kIdS = mma_idesc(128, kKvTile, false);
         constexpr uint32_t kIdO = mma_idesc(128, D, true);
+        constexpr uint32_t kTileUnits = S::kTileBytes >> 4;  // descriptor addresses count 16 bytes
+        const bool leader = elect_one();
+        const uint64_t qd = mma_desc(smem_u32(smem + S::kQ), 16, 1024);
+        const uint64_t kd = mma_desc(smem_u32(smem + S::kK), 16, 1024);
+        const uint64_t vd = mma_desc(smem_u32(smem + S::kV), 16384, 1024);
         auto qk = [&](int s, int slot) {
-          const uint32_t qa = smem_u32(smem + S::kQ + s * S::kTileBytes);
-          const uint32_t ka = smem_u32(smem + S::kK + slot * S::kTileBytes);
+          const uint64_t qa = qd + s * kTileUnits, ka = kd + slot * kTileUnits;
+          const uint32_t dst = tmem + s * 128;
+          if (leader) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-            mma_ss(tmem + s * 128, mma_desc(qa + off, 16, 1024), mma_desc(ka + off, 16, 1024), kIdS, k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
+              mma_ss(dst, qa + off, ka + off, kIdS, k > 0);
+            }
+            mma_commit(&sh.s_full[s]);
           }
-          mma_commit(&sh.s_full[s]);
         };
-        auto pv = [&](int s, int slot, bool first) {
-          const uint32_t va = smem_u32(smem + S::kV + slot * S::kTileBytes);
+        // step i of stream s: the first half of the tile's positions as soon as their weights
+        // are there
+        auto pv = [&](int s, int slot, int i) {
+          const uint64_t va = vd + slot * kTileUnits;
+          const uint32_t dst = tmem + 256 + s * D, src = tmem + s * 128;
+          if (!bar_wait(&sh.p_half[s], i & 1)) return false;
+          tc_fence_after();
+          if (leader) {
+            mma_ts(dst, src, va, kIdO, i > 0);
 #pragma unroll
-          for (int k = 0; k < kKvTile / 16; ++k)
-            mma_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8, mma_desc(va + k * 2048, 16384, 1024), kIdO,
-                   !first || k > 0);
+            for (int k = 1; k < kKvTile / 32; ++k) mma_ts(dst, src + k * 8, va + k * 128, kIdO, true);
+          }
+          if (!bar_wait(&sh.p_full[s], i & 1)) return false;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int k = kKvTile / 32; k < kKvTile / 16; ++k) mma_ts(dst, src + k * 8, va + k * 128, kIdO, true);
+          }
+          return true;
         };
+        auto commit = [&](uint64_t* bar) {
+          if (leader) mma_commit(bar);
+        };
+        ok = bar_wait(&sh.q_full, 0);
         if (shared_tiles) {
-          ok = bar_wait(&sh.k_full[0], 0);
+          ok = ok && bar_wait(&sh.k_full[0], 0);
           if (ok) {
             tc_fence_after();
             qk(0, 0);
             qk(1, 0);
-            mma_commit(&sh.k_empty[0]);
+            commit(&sh.k_empty[0]);
           }
           for (int t = 0; ok && t < tiles; ++t) {
             const int slot = t & 1, next = (t + 1) & 1;
             ok = bar_wait(&sh.v_full[slot], t >> 1 & 1);
             for (int s = 0; ok && s < 2; ++s) {
-              ok = bar_wait(&sh.p_full[s], t & 1);
+              ok = pv(s, slot, t);
               if (!ok) break;
-              tc_fence_after();
-              pv(s, slot, t == 0);
-              if (s == 1) mma_commit(&sh.v_empty[slot]);
+              if (s == 1) commit(&sh.v_empty[slot]);
               if (t + 1 < tiles) {
                 if (s == 0) {
                   ok = bar_wait(&sh.k_full[next], (t + 1) >> 1 & 1);
@@ -395,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
                   tc_fence_after();
                 }
                 qk(s, next);
-                if (s == 1) mma_commit(&sh.k_empty[next]);
+                if (s == 1) commit(&sh.k_empty[next]);
               }
             }
           }
@@ -405,30 +364,82 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
             if (!ok) break;
             tc_fence_after();
             qk(s, s);
-            mma_commit(&sh.k_empty[s]);
+            commit(&sh.k_empty[s]);
           }
           for (int t = 0; ok && t < tiles; ++t) {
             const int s = t & 1, i = t >> 1;
-            ok = bar_wait(&sh.v_full[s], i & 1) && bar_wait(&sh.p_full[s], i & 1);
+            ok = bar_wait(&sh.v_full[s], i & 1) && pv(s, s, i);
             if (!ok) break;
-            tc_fence_after();
-            pv(s, s, i == 0);
-            mma_commit(&sh.v_empty[s]);
+            commit(&sh.v_empty[s]);
             if (t + 2 < tiles) {
               ok = bar_wait(&sh.k_full[s], (i + 1) & 1);
               if (!ok) break;
               tc_fence_after();
               qk(s, s);
-              mma_commit(&sh.k_empty[s]);
+              commit(&sh.k_empty[s]);
             }
           }
         }
-        mma_commit(&sh.done);
+        commit(&sh.done);
+      }
+      if (warp == kCopyWarp) {
+        // -------------------------------------------------------------- copies
+        // codes and scales of the tiles in the order of the dequantizers, a half tile (64
+        // positions of one page) at a time, as far ahead as the staging ring allows
+        const uint8_t* kc = static_cast<const uint8_t*>(a.k_codes);
+        const uint8_t* ks = static_cast<const uint8_t*>(a.k_scales);
+        const uint8_t* vc = static_cast<const uint8_t*>(a.v_codes);
+        const uint8_t* vs = static_cast<const uint8_t*>(a.v_scales);
+        const int ps = a.desc.page_size;
+        // first cache row of 64-position block hb of the split, -1 for a page out of range
+        auto row_of = [&](int hb) -> int {
+          const int p = begin + hb * kTile;
+          if (p >= end) return -1;
+          const int pg = p / ps;
+          const int page = a.table ? __ldg(a.table + (int64_t)g * a.max_pages + pg) : g * a.max_pages + pg;
+          if (page < 0 || page >= a.desc.num_pages) {
+            set_flag(a.flags, KVQ_FLAG_BAD_PAGE);
+            return -1;
+          }
+          return (page * hkv + kvh) * ps + (p - pg * ps);
+        };
+        int krow = row_of(lane), vrow = krow;  // of blocks 32 i + lane, i the current window
+        int h = 0;
+        for (int t = -2; ok && t < tiles; ++t) {
+          for (int which = 0; ok && which < 2; ++which) {
+            const int tt = which ? t + 2 : t;
+            if (tt < 0 || tt >= tiles) continue;
+            for (int half = 0; ok && half < 2; ++half) {
+              const int hb = 2 * tt + half;
+              if (begin + hb * kTile >= end) break;
+              if ((hb & 31) == 0 && hb > 0) (which ? krow : vrow) = row_of(hb + lane);
+              const int row = __shfl_sync(0xffffffffu, which ? krow : vrow, hb & 31);
+              const int st = h % S::kStages;
+              ok = h < S::kStages || bar_wait(&sh.raw_empty[st], (h / S::kStages & 1) ^ 1);
+              if (!ok) break;
+              if (lane == 0) {
+                uint8_t* dst = smem + S::kRaw + st * S::kRawBytes;
+                if (row >= 0) {
+                  bar_expect(&sh.raw_full[st], S::kRawBytes);
+                  bulk_load(dst, (which ? kc : vc) + (int64_t)row * C::CROW, S::kRawCodes, &sh.raw_full[st]);
+                  bulk_load(dst + S::kRawCodes, (which ? ks : vs) + (int64_t)row * C::SROW, S::kRawScales,
+                            &sh.raw_full[st]);
+                } else {
+                  bar_arrive(&sh.raw_full[st]);  // whatever the stage holds: the call is flagged
+                }
+              }
+              ++h;
+            }
+          }
+        }
+        // no copy may land after the block has gone (each was waited for, unless a wait gave up)
+        for (int i = max(0, h - S::kStages); i < h; ++i) (void)bar_wait(&sh.raw_full[i % S::kStages], i / S::kStages & 1);
       }
       __syncwarp();
     } else if (warp >= kSoftmaxWarps) {
       // ---------------------------------------------------------------- dequantize
       // K0 K1 V0 K2 V1 K3 ...: the order in which the MMAs of either mode need the tiles
+      regs_shrink<kFillRegs>();
       const int ft = tid - 32 * kSoftmaxWarps;
       Lut lut;
       if constexpr (C::kLut || C::kNv) {
@@ -447,65 +458,91 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
           }
         }
       }
-      const uint8_t* kc = static_cast<const uint8_t*>(a.k_codes);
-      const uint8_t* ks = static_cast<const uint8_t*>(a.k_scales);
-      const uint8_t* vc = static_cast<const uint8_t*>(a.v_codes);
-      const uint8_t* vs = static_cast<const uint8_t*>(a.v_scales);
-      const int ps = a.desc.page_size;
-      // cache row of position p (a multiple of 64) of this unit's KV head; -1: none
-      auto base_of = [&](int p) -> int64_t {
-        if (p >= end) return -1;
-        const int pg = p / ps;
-        const int page = a.table ? __ldg(a.table + (int64_t)g * a.max_pages + pg) : g * a.max_pages + pg;
-        if (page < 0 || page >= a.desc.num_pages) {
-          set_flag(a.flags, KVQ_FLAG_BAD_PAGE);
-          return -1;
-        }
-        return ((int64_t)page * hkv + kvh) * ps + (p - pg * ps);
-      };
-      Fill<FMT, D> fk, fv;
-      auto load_k = [&](int t) {
+      // four warps per half tile; a half past the last position is filled with zeros
+      const int half = ft >> 7;
+      int staged = 0;  // half tiles staged before this tile's
+      auto put = [&](int t, uint8_t* slots, uint64_t* full, uint64_t* empty) {
         const int p = begin + t * kKvTile;
-        fill_load<FMT, D>(fk, kc, ks, base_of(p), base_of(p + 64), end - p, ft);
-      };
-      auto load_v = [&](int t) {
-        const int p = begin + t * kKvTile;
-        fill_load<FMT, D>(fv, vc, vs, base_of(p), base_of(p + 64), end - p, ft);
-      };
-      auto put_k = [&](int t) {
-        ok = t < 2 || bar_wait(&sh.k_empty[t & 1], (t >> 1 & 1) ^ 1);
+        const int n_half = p + kTile < end ? 2 : 1;
+        ok = t < 2 || bar_wait(&empty[t & 1], (t >> 1 & 1) ^ 1);
         if (!ok) return;
-        fill_store<FMT, D>(fk, smem + S::kK + (t & 1) * S::kTileBytes, ft, lut);
+        const int h = staged + half;
+        const uint8_t* raw = smem + S::kRaw + h % S::kStages * S::kRawBytes;
+        if (half < n_half) ok = bar_wait(&sh.raw_full[h % S::kStages], h / S::kStages & 1);
+        if (!ok) return;
+        fill_half<FMT, D>(raw, slots + (t & 1) * S::kTileBytes, half * kTile, end - p - half * kTile, ft & 127, lut);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) bar_arrive(&sh.k_full[t & 1]);
-      };
-      auto put_v = [&](int t) {
-        ok = t < 2 || bar_wait(&sh.v_empty[t & 1], (t >> 1 & 1) ^ 1);
-        if (!ok) return;
-        fill_store<FMT, D>(fv, smem + S::kV + (t & 1) * S::kTileBytes, ft, lut);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&sh.v_full[t & 1]);
-      };
-      load_k(0);
-      load_v(0);
-      put_k(0);
-      if (tiles > 1) {
-        load_k(1);
-        put_k(1);
-      }
-      if (tiles > 2) load_k(2);
-      for (int t = 0; ok && t < tiles; ++t) {
-        put_v(t);
-        if (t + 1 < tiles) load_v(t + 1);
-        if (ok && t + 2 < tiles) {
-          put_k(t + 2);
-          if (t + 3 < tiles) load_k(t + 3);
+        if (lane == 0) {
+          bar_arrive(&full[t & 1]);
+          if (half < n_half) bar_arrive(&sh.raw_empty[h % S::kStages]);
         }
+        staged += n_half;
+      };
+      for (int t = -2; ok && t < tiles; ++t) {
+        if (t >= 0) put(t, smem + S::kV, sh.v_full, sh.v_empty);
+        if (ok && t + 2 < tiles) put(t + 2, smem + S::kK, sh.k_full, sh.k_empty);
       }
     } else {
       // ---------------------------------------------------------------- softmax
+      regs_grow<kSoftmaxRegs>();
+      // query rows, fp16, K-major, 128-byte swizzle; rows past the unit's are zero
+        const __half* q = static_cast<const __half*>(a.q);
+        const bool zero = a.sm_scale == 0.f;
+        const uint32_t flip = a.sm_scale < 0.f ? 0x80008000u : 0u;  // the scale's sign goes into the query
+        if constexpr (!C::kLut) {
+          constexpr int kC = D / 8;
+          for (int i = tid; i < kRowTile * kC; i += 32 * kSoftmaxWarps) {
+            const int r = i / kC, c = i % kC;
+            const int rr = shared_tiles ? r : r & 127;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < rows && !zero) {
+              const int t = (row0 + rr) / G, h = (row0 + rr) % G;
+              v = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)(tok0 + t) * a.num_q_heads + kvh * G + h) * D) + c);
+              v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+            }
+            *reinterpret_cast<uint4*>(smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, c)) = v;
+          }
+        } else {
+          // rotated: (1/sqrt(D)) H (signs .* q); a warp per row, lane l holds E consecutive elements
+          constexpr int E = D / 32;
+          for (int r = warp; r < kRowTile; r += kSoftmaxWarps) {
+            const int rr = shared_tiles ? r : r & 127;
+            float y[E];
+    #pragma unroll
+            for (int k = 0; k < E; ++k) y[k] = 0.f;
+            if (rr < rows && !zero) {
+              const int t = (row0 + rr) / G, h = (row0 + rr) % G;
+              const __half* src = q + ((int64_t)(tok0 + t) * a.num_q_heads + kvh * G + h) * D + lane * E;
+    #pragma unroll
+              for (int k = 0; k < E; ++k) y[k] = __half2float(src[k]) * (float)a.desc.signs[lane * E + k];
+            }
+    #pragma unroll
+            for (int h = 1; h < E; h <<= 1)
+    #pragma unroll
+              for (int k = 0; k < E; ++k)
+                if (!(k & h)) {
+                  const float u = y[k], v = y[k + h];
+                  y[k] = u + v;
+                  y[k + h] = u - v;
+                }
+    #pragma unroll
+            for (int b = 1; b < 32; b <<= 1)
+    #pragma unroll
+              for (int k = 0; k < E; ++k) {
+                const float o = __shfl_xor_sync(0xffffffffu, y[k], b);
+                y[k] = (lane & b) ? o - y[k] : y[k] + o;
+              }
+            const float cs = D == 64 ? 0.125f : 0.08838834764831845f;  // 1/sqrt(D)
+            uint8_t* dst = smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, lane * E / 8) + (lane * E % 8) * 2;
+    #pragma unroll
+            for (int k = 0; k < E; k += 2)
+              *reinterpret_cast<uint32_t*>(dst + 2 * k) = pack_h2(y[k] * cs, y[k + 1] * cs) ^ flip;
+          }
+        }
+        fence_async_shared();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.q_full);
       const int s = warp >> 2;
       const int r = tid & 127;  // row of the row tile = TMEM lane
       const int rr = shared_tiles ? s * 128 + r : r;
@@ -522,20 +559,22 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
         tc_fence_after();
         const uint32_t ts = at + s * 128;
         const bool mask = __any_sync(0xffffffffu, lim < kKvTile);
-        // maximum
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int c = 0; c < kKvTile; c += 32) {
-          float v[32];
-          tmem_ld32(ts + c, v);
-          tmem_wait_ld32(v);
-          if (mask) {
+        float v[kKvTile];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = c + k < lim ? v[k] : -INFINITY;
-          }
+        for (int c = 0; c < kKvTile; c += 32) tmem_ld32(ts + c, v + c);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], v[k]);
+        for (int c = 0; c < kKvTile; c += 32) tmem_wait_ld32(v + c);
+        if (mask) {
+#pragma unroll
+          for (int k = 0; k < kKvTile; ++k) v[k] = k < lim ? v[k] : -INFINITY;
         }
+        float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int k = 4; k + 8 <= kKvTile; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], v[k + 2 * e], v[k + 2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], v[kKvTile - 4 + e]);
         const float tm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         const bool grow = tm > m + kRescaleBits || (m == -INFINITY && tm > -INFINITY);
         if (__any_sync(0xffffffffu, grow)) {
@@ -546,40 +585,48 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
           // accumulator is at rest
           if (i > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float v[32];
-              tmem_ld32(at + 256 + s * D + c, v);
-              tmem_wait_ld32(v);
+            for (int c = 0; c < D; c += 8) {
+              float o[8];
+              tmem_ld8(at + 256 + s * D + c, o);
+              tmem_wait_ld8(o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] *= f;
-              tmem_st32(at + 256 + s * D + c, reinterpret_cast<const uint32_t*>(v));
+              for (int k = 0; k < 8; ++k) o[k] *= f;
+              tmem_st8(at + 256 + s * D + c, o);
             }
             tmem_wait_st();
           }
         }
         const float off = m == -INFINITY ? 0.f : kWeightBits - m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int c = 0; c < kKvTile; c += 64) {
-          float v[64];
-          uint32_t p[32];
-          tmem_ld32(ts + c, v);
-          tmem_ld32(ts + c + 32, v + 32);
-          tmem_wait_ld32(v);
-          tmem_wait_ld32(v + 32);
-          if (mask) {
+        const uint64_t scale2 = pack_f2(scale, scale), off2 = pack_f2(off, off);
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of fp32 zeros
 #pragma unroll
-            for (int k = 0; k < 64; ++k) v[k] = c + k < lim ? v[k] : -INFINITY;
-          }
+        for (int c = 0; c < kKvTile; c += 64) {
+          uint32_t p[32];
 #pragma unroll
           for (int k = 0; k < 64; k += 2) {
-            const float e0 = ex2(fmaf(v[k], scale, off)), e1 = ex2(fmaf(v[k + 1], scale, off));
-            sum[(k >> 1) & 3] += e0 + e1;
+            const uint64_t x = fma_f2(pack_f2(v[c + k], v[c + k + 1]), scale2, off2);
+            float e0, e1;
+            if ((k >> 1) % 8 < kPolyPairs) {
+              exp2_poly(x, e0, e1);
+            } else {
+              unpack_f2(x, e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+            }
+            sum[(k >> 1) & 3] = add_f2(sum[(k >> 1) & 3], pack_f2(e0, e1));
             p[k >> 1] = pack_h2(e0, e1);
           }
           tmem_st32(ts + c / 2, p);
+          if (c == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sh.p_half[s]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float l0, l1;
+        unpack_f2(add_f2(add_f2(sum[0], sum[1]), add_f2(sum[2], sum[3])), l0, l1);
+        l += l0 + l1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -591,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
       m -= kWeightBits;  // the weights were 2^(s - m + 7)
       const float vscale = kUnhalve<FMT>;
       float f0 = vscale, f1 = 0.f;
-      float4* stage = reinterpret_cast<float4*>(smem + S::kK);  // [D / 4][128], stream 1's rows
+      float4* stage = reinterpret_cast<float4*>(smem + S::kV);  // [D / 4][128], stream 1's rows
       if (!shared_tiles) {
         // streams 0 and 1 hold the same rows: stream 1 hands its sums to stream 0
         if (s == 1) {
@@ -625,6 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
         const bool write = ok && rr < rows;
         const int64_t row = write ? (int64_t)(tok0 + (row0 + rr) / G) * a.num_q_heads + kvh * G + (row0 + rr) % G : 0;
         const int64_t part = row * a.splits + split;
+        // every tile has been read: the query and K / V space holds the rows
+        uint8_t* mine = smem + S::kQ + (s * 128 + r) * (D * 4 + 16);
         if (a.out) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
           f0 *= inv;
@@ -648,20 +697,26 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
             }
             v[k] = o.x; v[k + 1] = o.y; v[k + 2] = o.z; v[k + 3] = o.w;
           }
-          if (write) {
-            if (!a.out || !a.out_f16) {
-              float* dst = (a.out ? static_cast<float*>(a.out) + row * D : a.part_o + part * D) + c;
+          // the row's place in shared memory (16 bytes of padding between rows), then one copy
+          if (!a.out || !a.out_f16) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4*>(dst + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-            } else {
-              __half* dst = static_cast<__half*>(a.out) + row * D + c;
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(mine + (c + k) * 4) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          } else {
 #pragma unroll
-              for (int k = 0; k < 32; k += 8)
-                *reinterpret_cast<uint4*>(dst + k) = make_uint4(pack_h2(v[k], v[k + 1]), pack_h2(v[k + 2], v[k + 3]),
-                                                                pack_h2(v[k + 4], v[k + 5]), pack_h2(v[k + 6], v[k + 7]));
-            }
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(mine + (c + k) * 2) =
+                  make_uint4(pack_h2(v[k], v[k + 1]), pack_h2(v[k + 2], v[k + 3]), pack_h2(v[k + 4], v[k + 5]),
+                             pack_h2(v[k + 6], v[k + 7]));
           }
+        }
+        fence_async_shared();
+        if (write) {
+          const bool half = a.out && a.out_f16;
+          void* dst = half ? static_cast<void*>(static_cast<__half*>(a.out) + row * D)
+                           : static_cast<void*>((a.out ? static_cast<float*>(a.out) + row * D : a.part_o + part * D));
+          bulk_store(dst, mine, half ? D * 2 : D * 4);
+          bulk_store_wait();
         }
       }
     }
@@ -673,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
   }
   if (!ok) set_flag(a.flags, KVQ_FLAG_TIMEOUT);
   // the MMAs still in flight (after a wait that gave up) end before the TMEM is freed
-  if (warp == kMmaWarp && lane == 0 && live && tiles > 0) (void)bar_wait(&sh.done, 0);
+  if (warp == kMmaWarp && live && tiles > 0) (void)bar_wait(&sh.done, 0);
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -686,7 +741,7 @@ std::mutex g_rows_mu;
 
 template <int FMT, int D>
 int launch_t(const RowsArgs& a, cudaStream_t stream) {
-  constexpr int kBytes = Smem<D>::kBytes;
+  constexpr int kBytes = Smem<FMT, D>::kBytes;
   static uint64_t done_mask = 0;  // guarded by g_rows_mu
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
