@@ -41,8 +41,9 @@ constexpr int kSoftmaxWarps = 8, kFillWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps + kFillWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // a whole warpgroup for the MMA warp
 // Registers per thread by role, out of 96 x 640 at launch
-constexpr int kSoftmaxRegs = 168, kFillRegs = 56, kMmaRegs = 32;
-static_assert(256 * kSoftmaxRegs + 256 * kFillRegs + 128 * kMmaRegs <= 96 * kThreads, "register pool");
+constexpr int kSoftmaxRegs = 152, kFillRegs = 72, kMmaRegs = 32;
+static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kFillWarps * kFillRegs + 4 * kMmaRegs) <= 96 * kThreads,
+              "register pool");
 constexpr float kWeightBits = 7.f;   // weights are 2^(s - m + 7)
 constexpr float kRescaleBits = 8.f;  // growth of the maximum before the accumulator is rescaled
 #ifndef POLY
@@ -179,6 +180,7 @@ __device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8
 __device__ __forceinline__ void find_unit(const RowsArgs& a, int t, int lane, int* unit) {
   const int per = (a.num_groups + 31) / 32;
   const int g0 = min(lane * per, a.num_groups), g1 = min(g0 + per, a.num_groups);
+  const int len0 = g0 < g1 ? a.lens[g0] : 0;  // in flight with the offsets
   auto tokens = [&](int g, int& first) {
     if (!a.offsets) {
       first = 0;
@@ -192,8 +194,11 @@ __device__ __forceinline__ void find_unit(const RowsArgs& a, int t, int lane, in
     }
     return end - first;
   };
-  int mine = 0, first;
-  for (int g = g0; g < g1; ++g) mine += (tokens(g, first) * a.group + kRowTile - 1) / kRowTile;
+  int mine = 0, first = 0, n0 = 0;
+  for (int g = g0; g < g1; ++g) {
+    n0 = tokens(g, first);
+    mine += (n0 * a.group + kRowTile - 1) / kRowTile;
+  }
   int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -206,12 +211,12 @@ __device__ __forceinline__ void find_unit(const RowsArgs& a, int t, int lane, in
   if (t >= before && t < before + mine) {
     int k = t - before;
     for (int g = g0; g < g1; ++g) {
-      const int n = tokens(g, first);
+      const int n = per == 1 ? n0 : tokens(g, first);
       const int tiles = (n * a.group + kRowTile - 1) / kRowTile;
       if (k < tiles) {
         // the last rows of a causal group see the most positions: they start first
         const int tile = a.causal ? tiles - 1 - k : k;
-        int len = a.lens[g];
+        int len = g == g0 ? len0 : a.lens[g];
         if (len < 0 || len > a.max_len || len > (int64_t)a.max_pages * a.desc.page_size) {
           set_flag(a.flags, KVQ_FLAG_BAD_SEQLEN);
           len = 0;
@@ -486,61 +491,88 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
     } else {
       // ---------------------------------------------------------------- softmax
       regs_grow<kSoftmaxRegs>();
-      // query rows, fp16, K-major, 128-byte swizzle; rows past the unit's are zero
-        const __half* q = static_cast<const __half*>(a.q);
+      // query rows, fp16, K-major, 128-byte swizzle; rows past the unit's are zero.  The loads
+      // of several rows are in flight together.  A unit of one row tile fills both.
+      {
+        const __half* q = static_cast<const __half*>(a.q) + (int64_t)kvh * G * D;
         const bool zero = a.sm_scale == 0.f;
         const uint32_t flip = a.sm_scale < 0.f ? 0x80008000u : 0u;  // the scale's sign goes into the query
+        const int n_rows = shared_tiles ? kRowTile : 128;
+        auto src = [&](int r) {
+          const int t = (row0 + r) / G;
+          return q + ((int64_t)(tok0 + t) * a.num_q_heads + (row0 + r - t * G)) * D;
+        };
         if constexpr (!C::kLut) {
-          constexpr int kC = D / 8;
-          for (int i = tid; i < kRowTile * kC; i += 32 * kSoftmaxWarps) {
-            const int r = i / kC, c = i % kC;
-            const int rr = shared_tiles ? r : r & 127;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < rows && !zero) {
-              const int t = (row0 + rr) / G, h = (row0 + rr) % G;
-              v = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)(tok0 + t) * a.num_q_heads + kvh * G + h) * D) + c);
-              v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+          constexpr int kC = D / 8, kStep = 32 * kSoftmaxWarps / kC, kBatch = 8;
+          const int c = tid % kC;
+          for (int r0 = tid / kC; r0 < n_rows; r0 += kBatch * kStep) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int r = r0 + i * kStep;
+              v[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (r < rows && !zero) v[i] = __ldg(reinterpret_cast<const uint4*>(src(r)) + c);
             }
-            *reinterpret_cast<uint4*>(smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, c)) = v;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int r = r0 + i * kStep;
+              if (r >= n_rows) break;
+              v[i].x ^= flip; v[i].y ^= flip; v[i].z ^= flip; v[i].w ^= flip;
+              uint8_t* dst = smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, c);
+              *reinterpret_cast<uint4*>(dst) = v[i];
+              if (!shared_tiles) *reinterpret_cast<uint4*>(dst + S::kTileBytes) = v[i];
+            }
           }
         } else {
-          // rotated: (1/sqrt(D)) H (signs .* q); a warp per row, lane l holds E consecutive elements
-          constexpr int E = D / 32;
-          for (int r = warp; r < kRowTile; r += kSoftmaxWarps) {
-            const int rr = shared_tiles ? r : r & 127;
-            float y[E];
-    #pragma unroll
-            for (int k = 0; k < E; ++k) y[k] = 0.f;
-            if (rr < rows && !zero) {
-              const int t = (row0 + rr) / G, h = (row0 + rr) % G;
-              const __half* src = q + ((int64_t)(tok0 + t) * a.num_q_heads + kvh * G + h) * D + lane * E;
-    #pragma unroll
-              for (int k = 0; k < E; ++k) y[k] = __half2float(src[k]) * (float)a.desc.signs[lane * E + k];
+          // rotated: (1/sqrt(D)) H (signs .* q); D / 16 lanes per row, 16 elements each
+          constexpr int kL = D / 16, kR = 32 / kL;  // lanes per row, rows per warp
+          const int part = lane % kL;
+          float sg[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            sg[k] = (float)a.desc.signs[part * 16 + k] * (D == 64 ? 0.125f : 0.08838834764831845f);
+          for (int r = warp * kR + lane / kL; r < n_rows; r += kSoftmaxWarps * kR) {
+            uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+            if (r < rows && !zero) {
+              const uint4* p = reinterpret_cast<const uint4*>(src(r)) + part * 2;
+              raw[0] = __ldg(p);
+              raw[1] = __ldg(p + 1);
             }
-    #pragma unroll
-            for (int h = 1; h < E; h <<= 1)
-    #pragma unroll
-              for (int k = 0; k < E; ++k)
+            const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+            float y[16];
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float2 f = __half22float2(u32_as_h2(w[k / 2] ^ flip));
+              y[k] = f.x * sg[k];
+              y[k + 1] = f.y * sg[k + 1];
+            }
+#pragma unroll
+            for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
                 if (!(k & h)) {
-                  const float u = y[k], v = y[k + h];
-                  y[k] = u + v;
-                  y[k + h] = u - v;
+                  const float u = y[k], x = y[k + h];
+                  y[k] = u + x;
+                  y[k + h] = u - x;
                 }
-    #pragma unroll
-            for (int b = 1; b < 32; b <<= 1)
-    #pragma unroll
-              for (int k = 0; k < E; ++k) {
-                const float o = __shfl_xor_sync(0xffffffffu, y[k], b);
-                y[k] = (lane & b) ? o - y[k] : y[k] + o;
-              }
-            const float cs = D == 64 ? 0.125f : 0.08838834764831845f;  // 1/sqrt(D)
-            uint8_t* dst = smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, lane * E / 8) + (lane * E % 8) * 2;
-    #pragma unroll
-            for (int k = 0; k < E; k += 2)
-              *reinterpret_cast<uint32_t*>(dst + 2 * k) = pack_h2(y[k] * cs, y[k + 1] * cs) ^ flip;
+#pragma unroll
+            for (int b = 1; b < kL; b <<= 1) {
+              const float sign = (lane & b) ? -1.f : 1.f;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) y[k] = fmaf(y[k], sign, __shfl_xor_sync(0xffffffffu, y[k], b));
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float* z = y + 8 * c;
+              const uint4 h = make_uint4(pack_h2(z[0], z[1]), pack_h2(z[2], z[3]), pack_h2(z[4], z[5]), pack_h2(z[6], z[7]));
+              uint8_t* dst = smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, part * 2 + c);
+              *reinterpret_cast<uint4*>(dst) = h;
+              if (!shared_tiles) *reinterpret_cast<uint4*>(dst + S::kTileBytes) = h;
+            }
           }
         }
         fence_async_shared();
+      }
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.q_full);
       const int s = warp >> 2;
@@ -550,6 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
       const float scale = (a.sm_scale == 0.f ? 1.f : fabsf(a.sm_scale)) * kLog2e * kUnhalve<FMT>;
       const int limit = rr < rows ? min(row_limit(len, n, (row0 + rr) / G, a.causal), end) : end;
       const int steps = shared_tiles ? tiles : (tiles - s + 1) / 2;
+      const uint32_t ts = at + s * 128, to = at + 256 + s * D;  // scores, accumulator
+      const uint64_t scale2 = pack_f2(scale, scale);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < steps; ++i) {
         const int t = shared_tiles ? i : 2 * i + s;
@@ -557,7 +591,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
         ok = bar_wait(&sh.s_full[s], i & 1);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t ts = at + s * 128;
         const bool mask = __any_sync(0xffffffffu, lim < kKvTile);
         float v[kKvTile];
 #pragma unroll
@@ -587,17 +620,17 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 8) {
               float o[8];
-              tmem_ld8(at + 256 + s * D + c, o);
+              tmem_ld8(to + c, o);
               tmem_wait_ld8(o);
 #pragma unroll
               for (int k = 0; k < 8; ++k) o[k] *= f;
-              tmem_st8(at + 256 + s * D + c, o);
+              tmem_st8(to + c, o);
             }
             tmem_wait_st();
           }
         }
         const float off = m == -INFINITY ? 0.f : kWeightBits - m;
-        const uint64_t scale2 = pack_f2(scale, scale), off2 = pack_f2(off, off);
+        const uint64_t off2 = pack_f2(off, off);
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of fp32 zeros
 #pragma unroll
         for (int c = 0; c < kKvTile; c += 64) {
@@ -638,21 +671,21 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
       m -= kWeightBits;  // the weights were 2^(s - m + 7)
       const float vscale = kUnhalve<FMT>;
       float f0 = vscale, f1 = 0.f;
-      float4* stage = reinterpret_cast<float4*>(smem + S::kV);  // [D / 4][128], stream 1's rows
+      float4* stage = reinterpret_cast<float4*>(smem + S::kV) + r;  // [D / 4][128], stream 1's rows
       if (!shared_tiles) {
         // streams 0 and 1 hold the same rows: stream 1 hands its sums to stream 0
         if (s == 1) {
           sh.merge_m[r] = m;
           sh.merge_l[r] = l;
           if (steps > 0) {
-#pragma unroll 1
+#pragma unroll
             for (int c = 0; c < D; c += 32) {
               float v[32];
-              tmem_ld32(at + 256 + s * D + c, v);
+              tmem_ld32(to + c, v);
               tmem_wait_ld32(v);
 #pragma unroll
               for (int k = 0; k < 32; k += 4)
-                stage[(c + k) / 4 * 128 + r] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                stage[(c + k) / 4 * 128] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
             }
           }
         }
@@ -669,10 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
       }
       // every lane takes part in the TMEM loads; rows past the unit's are not written
       if (shared_tiles || s == 0) {
-        const bool write = ok && rr < rows;
+        const bool write = ok && rr < rows, half = a.out && a.out_f16;
         const int64_t row = write ? (int64_t)(tok0 + (row0 + rr) / G) * a.num_q_heads + kvh * G + (row0 + rr) % G : 0;
         const int64_t part = row * a.splits + split;
-        // every tile has been read: the query and K / V space holds the rows
+        // every tile has been read: the query and K / V space holds the rows (16 bytes of
+        // padding between them), each copied out by the thread that owns it
         uint8_t* mine = smem + S::kQ + (s * 128 + r) * (D * 4 + 16);
         if (a.out) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -682,39 +716,30 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
           a.part_m[part] = m;
           a.part_l[part] = l;
         }
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < D; c += 32) {
           float v[32];
-          tmem_ld32(at + 256 + s * D + c, v);
+          tmem_ld32(to + c, v);
           tmem_wait_ld32(v);
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
             float4 o = make_float4(v[k] * f0, v[k + 1] * f0, v[k + 2] * f0, v[k + 3] * f0);
             if (f1 != 0.f) {
-              const float4 x = stage[(c + k) / 4 * 128 + r];
+              const float4 x = stage[(c + k) / 4 * 128];
               o.x = fmaf(x.x, f1, o.x); o.y = fmaf(x.y, f1, o.y);
               o.z = fmaf(x.z, f1, o.z); o.w = fmaf(x.w, f1, o.w);
             }
-            v[k] = o.x; v[k + 1] = o.y; v[k + 2] = o.z; v[k + 3] = o.w;
-          }
-          // the row's place in shared memory (16 bytes of padding between rows), then one copy
-          if (!a.out || !a.out_f16) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(mine + (c + k) * 4) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; k += 8)
-              *reinterpret_cast<uint4*>(mine + (c + k) * 2) =
-                  make_uint4(pack_h2(v[k], v[k + 1]), pack_h2(v[k + 2], v[k + 3]), pack_h2(v[k + 4], v[k + 5]),
-                             pack_h2(v[k + 6], v[k + 7]));
+            if (half)
+              *reinterpret_cast<uint2*>(mine + (c + k) * 2) = make_uint2(pack_h2(o.x, o.y), pack_h2(o.z, o.w));
+            else
+              *reinterpret_cast<float4*>(mine + (c + k) * 4) = o;
           }
         }
         fence_async_shared();
         if (write) {
-          const bool half = a.out && a.out_f16;
-          void* dst = half ? static_cast<void*>(static_cast<__half*>(a.out) + row * D)
-                           : static_cast<void*>((a.out ? static_cast<float*>(a.out) + row * D : a.part_o + part * D));
+          uint8_t* dst = half    ? static_cast<uint8_t*>(a.out) + row * D * 2
+                         : a.out ? static_cast<uint8_t*>(a.out) + row * D * 4
+                                 : reinterpret_cast<uint8_t*>(a.part_o + part * D);
           bulk_store(dst, mine, half ? D * 2 : D * 4);
           bulk_store_wait();
         }

@@ -7,7 +7,7 @@
 namespace kvq {
 
 constexpr int kRowTile = 256;   // query rows of one unit (two TMEM row tiles of 128)
-constexpr int kKvTile = 128;    // positions of one K / V tile
+constexpr int kKvTile = 128;    // positions: one K / V block for each of two streams
 constexpr int kTargetCtas = 148;  // SMs of a B200: one CTA each
 
 // Attention of many query rows over groups of positions.  Group g owns the tokens
