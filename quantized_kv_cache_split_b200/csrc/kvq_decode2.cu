@@ -274,14 +274,6 @@ __device__ __forceinline__ void vg_lut(const uint8_t* __restrict__ codes, const 
     mma16816(acc[mt], eab[2 * mt], eab[2 * mt + 1], ecd[2 * mt], ecd[2 * mt + 1], p01, p89);
 }
 
-// An 8x8 matrix of 16-bit elements held one row pair per lane (lane (r, c): row r,
-// columns 2c, 2c + 1), transposed: lane (r, c) gets row 2c and 2c + 1 of column r.
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 // ------------------------------------------------------------------ exchange publication
 // The split's (m, l) of every head (lane h holds head h) stored by lane 0, then its
 // arrival on the (sequence, KV head)'s arrival word; returns (in lane 0) the count that

@@ -69,6 +69,14 @@ __device__ __forceinline__ void ldsm_x4_trans(const void* p, uint32_t& d0, uint3
                : "memory");
 }
 
+// An 8x8 matrix of 16-bit elements held one row pair per lane (lane (r, c): row r,
+// columns 2c, 2c + 1), transposed: lane (r, c) gets row 2c and 2c + 1 of column r.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // ------------------------------------------------------------------ thread-block clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;

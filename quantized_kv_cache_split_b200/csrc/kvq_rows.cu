@@ -30,7 +30,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "kvq_decode_common.cuh"
+#include "kvq_own.cuh"
 #include "kvq_rows.h"
 #include "kvq_tcgen05.cuh"
 
@@ -44,6 +44,8 @@ constexpr int kThreads = 32 * (kMmaWarp + 4);  // a whole warpgroup for the MMA 
 constexpr int kSoftmaxRegs = 152, kFillRegs = 72, kMmaRegs = 32;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kFillWarps * kFillRegs + 4 * kMmaRegs) <= 96 * kThreads,
               "register pool");
+constexpr int kOwnWarps = 12, kOwnRegs = 136;  // blocks of own units: three warpgroups of five
+static_assert(32 * (kOwnWarps * kOwnRegs + (kThreads / 32 - kOwnWarps) * kMmaRegs) <= 96 * kThreads, "register pool");
 constexpr float kWeightBits = 7.f;   // weights are 2^(s - m + 7)
 constexpr float kRescaleBits = 8.f;  // growth of the maximum before the accumulator is rescaled
 #ifndef POLY
@@ -83,6 +85,7 @@ struct Smem {
   static constexpr int kBars = kRaw + kStages * kRawBytes;
   static constexpr int kBytes = kBars + (int)sizeof(Shared) + 1024;  // slack: 1024-byte alignment
   static_assert(256 * (D * 4 + 16) <= kRaw && 128 * (D * 4 + 16) <= kV, "room for the results");
+  static_assert(kOwnWarps * Own<FMT, D>::kBytes <= kBars, "room for the own units");
   static_assert(kStages >= 3 && kBars % 16 == 0 && kRawCodes % 128 == 0 && kRawScales % 16 == 0, "staging");
 };
 
@@ -237,7 +240,7 @@ __device__ __forceinline__ void find_unit(const RowsArgs& a, int t, int lane, in
 
 // ------------------------------------------------------------------ the kernel
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, const OwnArgs own) {
   using C = Cfg<FMT, D>;
   using S = Smem<FMT, D>;
   extern __shared__ uint8_t raw_smem[];
@@ -245,6 +248,19 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
   Shared& sh = *reinterpret_cast<Shared*>(smem + S::kBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hkv = a.desc.num_kv_heads, G = a.group;
+  grid_dependents_launch();  // the merge may be scheduled (it waits for this grid's results)
+  const int row_blocks = a.row_tiles * hkv * a.splits;
+  if ((int)blockIdx.x >= row_blocks) {
+    // the requests' own positions: twelve warps, a unit each
+    if (warp < kOwnWarps) {
+      regs_grow<kOwnRegs>();
+      const int64_t u = (int64_t)(blockIdx.x - row_blocks) * kOwnWarps + warp;
+      if (u < own.units) own_unit<FMT, D>(own, a, u, smem + warp * Own<FMT, D>::kBytes, lane);
+    } else {
+      regs_shrink<kMmaRegs>();
+    }
+    return;
+  }
   // block: split fastest, then KV head, then row tile
   const int split = blockIdx.x % a.splits;
   const int kvh = blockIdx.x / a.splits % hkv;
@@ -765,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a) {
 std::mutex g_rows_mu;
 
 template <int FMT, int D>
-int launch_t(const RowsArgs& a, cudaStream_t stream) {
+int launch_t(const RowsArgs& a, const OwnArgs& own, cudaStream_t stream) {
   constexpr int kBytes = Smem<FMT, D>::kBytes;
   static uint64_t done_mask = 0;  // guarded by g_rows_mu
   int dev = 0;
@@ -778,10 +794,11 @@ int launch_t(const RowsArgs& a, cudaStream_t stream) {
       done_mask |= 1ull << dev;
     }
   }
-  const int64_t blocks = (int64_t)a.row_tiles * a.desc.num_kv_heads * a.splits;
+  const int64_t blocks =
+      (int64_t)a.row_tiles * a.desc.num_kv_heads * a.splits + (own.units + kOwnWarps - 1) / kOwnWarps;
   if (blocks <= 0) return KVQ_OK;
   if (blocks > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
-  rows_kernel<FMT, D><<<(unsigned)blocks, kThreads, kBytes, stream>>>(a);
+  rows_kernel<FMT, D><<<(unsigned)blocks, kThreads, kBytes, stream>>>(a, own);
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
@@ -789,12 +806,12 @@ int launch_t(const RowsArgs& a, cudaStream_t stream) {
 
 // One CTA per SM: a unit is cut along its positions until the units fill the device, in
 // pieces of at least two tiles (one per stream when the rows fit one row tile).
-RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, int max_len) {
+RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, int max_len, int ctas) {
   RowsPlan p;
   const int64_t rows = (int64_t)n_tokens * group;
   p.row_tiles = (int)((rows + (int64_t)num_groups * (kRowTile - 1)) / kRowTile);
   const int64_t units = std::max<int64_t>(1, (int64_t)p.row_tiles * num_kv_heads);
-  const int64_t want = std::max<int64_t>(1, kTargetCtas / units);
+  const int64_t want = std::max<int64_t>(1, ctas / units);
   const int64_t len = std::max(max_len, 1);
   int64_t chunk = (len + want - 1) / want;
   chunk = std::max<int64_t>((chunk + kKvTile - 1) / kKvTile * kKvTile, 2 * kKvTile);
@@ -803,21 +820,32 @@ RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, in
   return p;
 }
 
+// A warp per split, as many splits as the device holds warps of own units, whole blocks.
+int plan_own(int num_kv_heads, int batch, int max_seq_len, int* ctas) {
+  const int64_t pairs = (int64_t)std::max(batch, 1) * num_kv_heads;
+  const int64_t slots = (int64_t)kTargetCtas * kOwnWarps;
+  const int64_t l = (pairs * max_seq_len + slots - 1) / slots;
+  const int split = (int)std::max<int64_t>((l + kTile - 1) / kTile * kTile, kTile);
+  const int64_t units = pairs * ((max_seq_len + split - 1) / split);
+  *ctas = (int)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, 0x7fffffff);
+  return split;
+}
+
 size_t rows_partial_bytes(int n_tokens, int num_q_heads, int head_dim, int splits) {
   const size_t n = (size_t)n_tokens * num_q_heads * splits;
   return n * ((size_t)head_dim + 2) * sizeof(float);
 }
 
-int launch_rows(const RowsArgs& a, cudaStream_t stream) {
+int launch_rows(const RowsArgs& a, const OwnArgs& own, cudaStream_t stream) {
   const int f = a.desc.fmt, d = a.desc.head_dim;
-  if (f == KVQ_FMT_Q8_0 && d == 128) return launch_t<KVQ_FMT_Q8_0, 128>(a, stream);
-  if (f == KVQ_FMT_Q8_0 && d == 64) return launch_t<KVQ_FMT_Q8_0, 64>(a, stream);
-  if (f == KVQ_FMT_Q4_0 && d == 128) return launch_t<KVQ_FMT_Q4_0, 128>(a, stream);
-  if (f == KVQ_FMT_Q4_0 && d == 64) return launch_t<KVQ_FMT_Q4_0, 64>(a, stream);
-  if (f == KVQ_FMT_LUT4 && d == 128) return launch_t<KVQ_FMT_LUT4, 128>(a, stream);
-  if (f == KVQ_FMT_LUT4 && d == 64) return launch_t<KVQ_FMT_LUT4, 64>(a, stream);
-  if (f == KVQ_FMT_NVFP4 && d == 128) return launch_t<KVQ_FMT_NVFP4, 128>(a, stream);
-  if (f == KVQ_FMT_NVFP4 && d == 64) return launch_t<KVQ_FMT_NVFP4, 64>(a, stream);
+  if (f == KVQ_FMT_Q8_0 && d == 128) return launch_t<KVQ_FMT_Q8_0, 128>(a, own, stream);
+  if (f == KVQ_FMT_Q8_0 && d == 64) return launch_t<KVQ_FMT_Q8_0, 64>(a, own, stream);
+  if (f == KVQ_FMT_Q4_0 && d == 128) return launch_t<KVQ_FMT_Q4_0, 128>(a, own, stream);
+  if (f == KVQ_FMT_Q4_0 && d == 64) return launch_t<KVQ_FMT_Q4_0, 64>(a, own, stream);
+  if (f == KVQ_FMT_LUT4 && d == 128) return launch_t<KVQ_FMT_LUT4, 128>(a, own, stream);
+  if (f == KVQ_FMT_LUT4 && d == 64) return launch_t<KVQ_FMT_LUT4, 64>(a, own, stream);
+  if (f == KVQ_FMT_NVFP4 && d == 128) return launch_t<KVQ_FMT_NVFP4, 128>(a, own, stream);
+  if (f == KVQ_FMT_NVFP4 && d == 64) return launch_t<KVQ_FMT_NVFP4, 64>(a, own, stream);
   return KVQ_ERR_UNSUPPORTED;
 }
 

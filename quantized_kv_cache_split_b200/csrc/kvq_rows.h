@@ -40,28 +40,32 @@ struct RowsArgs {
   uint32_t* flags;
 };
 
+// Decode of single tokens over their own positions in the same launch (kvq_own.cuh): token b's
+// positions 0 .. seq_lens[b] - 1, cut at multiples of split.  units = 0: none.
+struct OwnArgs {
+  int64_t units;           // n_tokens * num_kv_heads * max_splits, one warp each
+  const int32_t* table;    // [n_tokens][max_pages], or null: pages b*max_pages ..
+  int max_pages;
+  const int32_t* seq_lens;
+  int max_seq_len, split, max_splits;
+  float* part_o;           // [n_tokens][num_q_heads][max_splits][head_dim], unnormalized
+  float* part_m;           // [n_tokens][num_q_heads][max_splits] maximum, log2 units
+  float* part_l;
+};
+
 // The split of a request: row tiles, splits and positions per split.
 struct RowsPlan {
   int row_tiles, splits, chunk;
 };
-RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, int max_len);
+RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, int max_len, int ctas);
 size_t rows_partial_bytes(int n_tokens, int num_q_heads, int head_dim, int splits);
+// Positions per split of the own part, and the CTAs it takes.
+int plan_own(int num_kv_heads, int batch, int max_seq_len, int* ctas);
 
-int launch_rows(const RowsArgs& a, cudaStream_t stream);
-
-// Merge of the partials of a rows launch and, when seq_lens is given, of a decode launch
-// (one token per request, same rows) into the normalized output; lut4 is rotated back.
-struct MergeArgs {
-  RowsArgs rows;
-  const int32_t* seq_lens;  // own positions of each token's request, or null
-  int max_seq_len, split_tokens, max_splits;
-  const float* own_o;       // [n_tokens][num_q_heads][max_splits][head_dim]
-  const float* own_m;
-  const float* own_l;
-  void* out;
-  int out_f16;
-};
-int launch_rows_merge(const MergeArgs& a, cudaStream_t stream);
+int launch_rows(const RowsArgs& a, const OwnArgs& own, cudaStream_t stream);
+// Merge of the partials of a rows launch (own.units > 0: those of the own positions as well)
+// into the normalized output; lut4 is rotated back.
+int launch_rows_merge(const RowsArgs& a, const OwnArgs& own, void* out, int out_f16, cudaStream_t stream);
 
 // The visible positions of token i of a group of n tokens and `len` positions.
 __host__ __device__ inline int row_limit(int len, int n, int i, int causal) {

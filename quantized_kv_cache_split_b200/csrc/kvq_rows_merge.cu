@@ -22,24 +22,37 @@ __device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
   }
 }
 
-// Add n partials (consecutive in o, m, l) under the maximum M.
+struct MergeArgs {
+  RowsArgs rows;
+  OwnArgs own;
+  void* out;
+  int out_f16;
+};
+
+// Add n partials (consecutive in o, m, l) under the maximum M; mine: this lane's m (of partial
+// `lane`) of the first 32.
 template <int E>
 __device__ __forceinline__ void add_partials(const float* __restrict__ o, const float* __restrict__ m,
-                                             const float* __restrict__ l, int n, float M, int lane,
+                                             const float* __restrict__ l, int n, float M, float mine, int lane,
                                              float (&acc)[E], float& den) {
   constexpr int D = 32 * E;
+  constexpr int kBatch = 8;  // reads in flight
   for (int base = 0; base < n; base += 32) {
     const int k = min(32, n - base);
-    const float w = lane < k ? ex2(m[base + lane] - M) : 0.f;
+    if (base > 0) mine = lane < k ? m[base + lane] : -INFINITY;
+    const float w = lane < k ? ex2(mine - M) : 0.f;
     if (lane < k) den = fmaf(w, l[base + lane], den);
-#pragma unroll 4
-    for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      float v[E];
-      load_row<E>(o + (int64_t)(base + i) * D + lane * E, v);
-      if (wi != 0.f) {
+    for (int i = 0; i < k; i += kBatch) {
+      float v[kBatch][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, v[e], acc[e]);
+      for (int t = 0; t < kBatch; ++t) load_row<E>(o + (int64_t)(base + min(i + t, k - 1)) * D + lane * E, v[t]);
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) {
+        const float wi = __shfl_sync(0xffffffffu, w, (i + t) & 31);
+        if (i + t < k && wi != 0.f) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, v[t][e], acc[e]);
+        }
       }
     }
   }
@@ -53,14 +66,20 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergeArgs
   const RowsArgs& r = a.rows;
   if (row >= (int64_t)r.n_tokens * r.num_q_heads) return;
   const int token = (int)(row / r.num_q_heads);
-  // the token's group: the last one whose first token is not behind it
+  // the token's group: the last one whose first token is not behind it (32 candidates at a time)
   int g = 0, first = 0, n = r.n_tokens;
   bool found = r.num_groups > 0;
   if (r.offsets) {
-    int lo = 0, hi = r.num_groups;
+    int lo = 0, hi = r.num_groups;  // offsets[lo] <= token (or lo = 0), the answer in lo .. hi
     while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (r.offsets[mid] <= token) lo = mid; else hi = mid - 1;
+      const int step = (hi - lo + 31) / 32;
+      const int at = min(lo + (lane + 1) * step, hi);
+      const uint32_t le = __ballot_sync(0xffffffffu, r.offsets[at] <= token);
+      const int k = __popc(le);  // the offsets do not decrease
+      const int nlo = k == 0 ? lo : min(lo + k * step, hi);
+      hi = k == 32 ? hi : min(lo + (k + 1) * step, hi) - 1;
+      lo = nlo;
+      if (hi < lo) hi = lo;
     }
     g = lo;
     found = g < r.num_groups;
@@ -70,32 +89,35 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergeArgs
       found = first >= 0 && token >= first && token < first + n && first + n <= r.n_tokens;
     }
   }
-  if (!found && !a.seq_lens) return;  // a token behind the last request: left as it was
-  int ns = 0;
+  int ns = 0, no = 0;
   if (found) {
     int len = r.lens[g];
     if (len < 0 || len > r.max_len || len > (int64_t)r.max_pages * r.desc.page_size) len = 0;
     const int lim = min(len, row_limit(len, n, token - first, r.causal));
     ns = (int)(((int64_t)lim + r.chunk - 1) / r.chunk);
   }
-  int no = 0;
-  if (a.seq_lens) {
-    const int len = max(0, min(a.seq_lens[token], a.max_seq_len));
-    no = (len + a.split_tokens - 1) / a.split_tokens;
+  if (a.own.units > 0) {
+    int len = a.own.seq_lens[token];
+    if (len < 0 || len > a.own.max_seq_len || len > (int64_t)a.own.max_pages * r.desc.page_size) len = 0;
+    no = (len + a.own.split - 1) / a.own.split;
   }
+  grid_dependency_wait();  // the partials
+  if (!found && a.own.units == 0) return;  // a token behind the last request: left as it was
   const float* pm = r.part_m + row * r.splits;
-  const float* om = a.own_m + row * a.max_splits;
-  float M = -INFINITY;
-  for (int i = lane; i < ns; i += 32) M = fmaxf(M, pm[i]);
-  for (int i = lane; i < no; i += 32) M = fmaxf(M, om[i]);
+  const float* om = a.own.part_m + row * a.own.max_splits;
+  const float m0 = lane < ns ? pm[lane] : -INFINITY, m1 = lane < no ? om[lane] : -INFINITY;
+  float M = fmaxf(m0, m1);
+  for (int i = lane + 32; i < ns; i += 32) M = fmaxf(M, pm[i]);
+  for (int i = lane + 32; i < no; i += 32) M = fmaxf(M, om[i]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[E], den = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   if (M != -INFINITY) {
-    add_partials<E>(r.part_o + row * r.splits * D, pm, r.part_l + row * r.splits, ns, M, lane, acc, den);
-    add_partials<E>(a.own_o + row * a.max_splits * D, om, a.own_l + row * a.max_splits, no, M, lane, acc, den);
+    add_partials<E>(r.part_o + row * r.splits * D, pm, r.part_l + row * r.splits, ns, M, m0, lane, acc, den);
+    add_partials<E>(a.own.part_o + row * a.own.max_splits * D, om, a.own.part_l + row * a.own.max_splits, no, M, m1,
+                    lane, acc, den);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -140,21 +162,28 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergeArgs
 
 }  // namespace
 
-int launch_rows_merge(const MergeArgs& a, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.rows.n_tokens * a.rows.num_q_heads;
+int launch_rows_merge(const RowsArgs& r, const OwnArgs& own, void* out, int out_f16, cudaStream_t stream) {
+  const int64_t rows = (int64_t)r.n_tokens * r.num_q_heads;
   if (rows <= 0) return KVQ_OK;
   const int64_t blocks = (rows + kMergeWarps - 1) / kMergeWarps;
   if (blocks > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
-  const bool rot = a.rows.desc.fmt == KVQ_FMT_LUT4;
-  const unsigned n = (unsigned)blocks;
-  if (a.rows.desc.head_dim == 128) {
-    if (rot) merge_kernel<128, true><<<n, 32 * kMergeWarps, 0, stream>>>(a);
-    else merge_kernel<128, false><<<n, 32 * kMergeWarps, 0, stream>>>(a);
-  } else {
-    if (rot) merge_kernel<64, true><<<n, 32 * kMergeWarps, 0, stream>>>(a);
-    else merge_kernel<64, false><<<n, 32 * kMergeWarps, 0, stream>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  const MergeArgs a{r, own, out, out_f16};
+  // scheduled while the rows launch still runs; it waits for it on the device
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+  cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool rot = r.desc.fmt == KVQ_FMT_LUT4;
+  const cudaError_t st = r.desc.head_dim == 128 ? (rot ? cudaLaunchKernelEx(&cfg, merge_kernel<128, true>, a)
+                                                       : cudaLaunchKernelEx(&cfg, merge_kernel<128, false>, a))
+                                                : (rot ? cudaLaunchKernelEx(&cfg, merge_kernel<64, true>, a)
+                                                       : cudaLaunchKernelEx(&cfg, merge_kernel<64, false>, a));
+  return st == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // namespace kvq

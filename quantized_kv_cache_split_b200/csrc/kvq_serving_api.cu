@@ -32,12 +32,21 @@ bool needs_merge(const kvq_cache_desc* desc, const RowsPlan& p) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Positions per split of the requests' own part of prefix decode: about one split per CTA
-// slot (four CTAs of four warps per SM), 128 to 512 positions.
-int own_split(const kvq_cache_desc* desc, int batch, int max_seq_len) {
-  const int64_t pairs = (int64_t)std::max(batch, 1) * desc->num_kv_heads;
-  const int64_t l = (pairs * max_seq_len + 4 * kTargetCtas - 1) / (4 * kTargetCtas);
-  return (int)std::min<int64_t>(std::max<int64_t>((l + kTile - 1) / kTile * kTile, 128), 512);
+// The two parts of prefix decode: how each is cut.  The prefix gets the CTAs that the own part
+// leaves, when that is most of them.
+struct PrefixPlan {
+  RowsPlan rows;
+  int own_split, own_splits;
+};
+PrefixPlan plan_prefix(const kvq_cache_desc* desc, int batch, int num_q_heads, int num_groups, int max_prefix_len,
+                       int max_seq_len) {
+  PrefixPlan p;
+  int ctas = 0;
+  p.own_split = plan_own(desc->num_kv_heads, batch, max_seq_len, &ctas);
+  p.own_splits = (max_seq_len + p.own_split - 1) / p.own_split;
+  p.rows = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, batch, num_groups, max_prefix_len,
+                     ctas <= kTargetCtas / 4 ? kTargetCtas - ctas : kTargetCtas);
+  return p;
 }
 
 // Pointers into a rows workspace at `at`.
@@ -95,7 +104,7 @@ int kvq_plan_step(int32_t batch, int32_t page_size, int32_t num_pages, int32_t m
 size_t kvq_prompt_workspace_size(const kvq_cache_desc* desc, int32_t n_tokens, int32_t num_q_heads,
                                  int32_t batch, int32_t max_seq_len) {
   if (check_rows(desc, n_tokens, num_q_heads, batch, max_seq_len) != KVQ_OK) return 0;
-  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len);
+  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len, kTargetCtas);
   return kWorkspaceHeader +
          (needs_merge(desc, p) ? rows_partial_bytes(n_tokens, num_q_heads, desc->head_dim, p.splits) : 0);
 }
@@ -104,10 +113,9 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
                                  int32_t num_groups, int32_t max_prefix_len, int32_t max_seq_len) {
   if (check_rows(desc, batch, num_q_heads, num_groups, max_prefix_len) != KVQ_OK) return 0;
   if (batch > KVQ_MAX_BATCH || max_seq_len < 0 || max_seq_len > kMaxLen) return 0;
-  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, batch, num_groups, max_prefix_len);
-  return round256(kvq_workspace_size(batch, num_q_heads, desc->head_dim, max_seq_len,
-                                     own_split(desc, batch, max_seq_len))) +
-         rows_partial_bytes(batch, num_q_heads, desc->head_dim, p.splits);
+  const PrefixPlan p = plan_prefix(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len);
+  return kWorkspaceHeader + round256(rows_partial_bytes(batch, num_q_heads, desc->head_dim, p.rows.splits)) +
+         rows_partial_bytes(batch, num_q_heads, desc->head_dim, p.own_splits);
 }
 
 int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
@@ -131,10 +139,10 @@ int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
   if (workspace_bytes < kvq_prompt_workspace_size(desc, n_tokens, num_q_heads, batch, max_seq_len))
     return KVQ_ERR_WORKSPACE;
   if (batch == 0 || n_tokens == 0) return KVQ_OK;
-  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len);
+  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len, kTargetCtas);
   const bool merge = needs_merge(desc, p);
-  MergeArgs m{};
-  RowsArgs& r = m.rows;
+  RowsArgs r{};
+  const OwnArgs own{};
   r.desc = *desc;
   r.q = q;
   r.n_tokens = n_tokens;
@@ -160,11 +168,9 @@ int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
   else r.out = out;
   r.out_f16 = out_type == KVQ_OUT_F16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = launch_rows(r, s);
+  st = launch_rows(r, own, s);
   if (st != KVQ_OK || !merge) return st;
-  m.out = out;
-  m.out_f16 = r.out_f16;
-  return launch_rows_merge(m, s);
+  return launch_rows_merge(r, own, out, r.out_f16, s);
 }
 
 int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_t num_q_heads,
@@ -188,17 +194,13 @@ int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, in
   if (!group_offsets && num_groups != 1) return KVQ_ERR_INVALID_ARG;
   if (!prefix_table && (int64_t)num_groups * max_prefix_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
   if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
-  const int L = own_split(desc, batch, max_seq_len);
-  const int max_splits = (max_seq_len + L - 1) / L;
-  if (batch > KVQ_MAX_BATCH || max_seq_len > kMaxLen || max_splits > KVQ_MAX_SPLITS) return KVQ_ERR_UNSUPPORTED;
+  if (batch > KVQ_MAX_BATCH || max_seq_len > kMaxLen) return KVQ_ERR_UNSUPPORTED;
   if (workspace_bytes < kvq_prefix_workspace_size(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len))
     return KVQ_ERR_WORKSPACE;
   if (batch == 0) return KVQ_OK;
-  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, batch, num_groups, max_prefix_len);
+  const PrefixPlan p = plan_prefix(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t own_bytes = kvq_workspace_size(batch, num_q_heads, desc->head_dim, max_seq_len, L);
-  MergeArgs m{};
-  RowsArgs& r = m.rows;
+  RowsArgs r{};
   r.desc = *desc;
   r.q = q;
   r.n_tokens = batch;
@@ -216,31 +218,28 @@ int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, in
   r.num_groups = num_groups;
   r.causal = 0;
   r.sm_scale = sm_scale;
-  r.splits = p.splits;
-  r.chunk = p.chunk;
-  r.row_tiles = p.row_tiles;
+  r.splits = p.rows.splits;
+  r.chunk = p.rows.chunk;
+  r.row_tiles = max_prefix_len > 0 ? p.rows.row_tiles : 0;
   r.flags = reinterpret_cast<uint32_t*>(ws);
-  set_partials(&r, ws + round256(own_bytes));
+  set_partials(&r, ws + kWorkspaceHeader);
+  OwnArgs own{};
+  own.max_splits = p.own_splits;
+  own.units = (int64_t)batch * desc->num_kv_heads * p.own_splits;
+  own.table = page_table;
+  own.max_pages = max_pages;
+  own.seq_lens = seq_lens;
+  own.max_seq_len = max_seq_len;
+  own.split = p.own_split;
+  const size_t n_own = (size_t)batch * num_q_heads * p.own_splits;
+  own.part_o = reinterpret_cast<float*>(
+      ws + kWorkspaceHeader + round256(rows_partial_bytes(batch, num_q_heads, desc->head_dim, p.rows.splits)));
+  own.part_m = own.part_o + n_own * desc->head_dim;
+  own.part_l = own.part_m + n_own;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // the requests' own positions: the decode kernel, its partials left in the workspace
-  st = kvq_decode_attn(desc, q, batch, num_q_heads, k_codes, k_scales, v_codes, v_scales, page_table, max_pages,
-                       seq_lens, max_seq_len, sm_scale, 0.f, L, 0u, workspace, own_bytes, nullptr, nullptr, stream);
+  st = launch_rows(r, own, s);
   if (st != KVQ_OK) return st;
-  if (max_prefix_len > 0) {
-    st = launch_rows(r, s);
-    if (st != KVQ_OK) return st;
-  }
-  m.seq_lens = seq_lens;
-  m.max_seq_len = max_seq_len;
-  m.split_tokens = L;
-  m.max_splits = max_splits;
-  const size_t n_own = (size_t)batch * num_q_heads * max_splits;
-  m.own_o = reinterpret_cast<const float*>(ws + kWorkspaceHeader + counters_bytes(batch, num_q_heads) + 16 * n_own);
-  m.own_m = m.own_o + n_own * desc->head_dim;
-  m.own_l = m.own_m + n_own;
-  m.out = out;
-  m.out_f16 = out_type == KVQ_OUT_F16;
-  return launch_rows_merge(m, s);
+  return launch_rows_merge(r, own, out, out_type == KVQ_OUT_F16, s);
 }
 
 }  // extern "C"
