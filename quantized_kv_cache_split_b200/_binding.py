@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -94,13 +95,9 @@ def _load():
         "kvq_decode_attn_noalloc": (ctypes.c_int, [D, P, I32, I32, P, P, P, P, P, I32, P, I32, F32,
                                                    F32, I32, U32, P, P, P]),
         "kvq_noalloc_read_flags": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), P]),
-        "kvq_plan_step": (ctypes.c_int, [I32] * 5 + [P] * 11 + [SZ, P]),
+        "kvq_packed_call": (ctypes.c_int, [I32, ctypes.c_char_p]),
         "kvq_prompt_workspace_size": (SZ, [D, I32, I32, I32, I32]),
         "kvq_prefix_workspace_size": (SZ, [D, I32, I32, I32, I32, I32]),
-        "kvq_prompt_attn": (ctypes.c_int, [D, P, I32, I32, P, P, P, P, P, I32, P, I32, P, I32, I32,
-                                           F32, P, SZ, P, I32, P]),
-        "kvq_prefix_attn": (ctypes.c_int, [D, P, I32, I32, P, P, P, P, P, I32, P, I32, P, I32, P,
-                                           I32, P, I32, F32, P, SZ, P, I32, P]),
         "kvq_lloyd_max_codebook": (ctypes.c_int, [I32, ctypes.c_double,
                                                   ctypes.POINTER(ctypes.c_uint16)]),
         "kvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -277,15 +274,36 @@ def kvq_noalloc_read_flags(stream=None) -> int:
     return int(flags.value)
 
 
+# kvq_plan_step, kvq_prompt_attn and kvq_prefix_attn take their many arguments as one block of
+# 64-bit words (ctypes converts arguments one by one, at a third of a microsecond each).
+_PLAN = struct.Struct("=18q")
+_PROMPT = struct.Struct("=15qd5q")
+_PREFIX = struct.Struct("=18qd5q")
+
+
+def _i32(x: int) -> int:
+    """An integer argument; one that an int32 cannot hold is refused here, not cut."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise KvqError("integer argument", KVQ_ERR_INVALID_ARG)
+    return x
+
+
+def _word(t) -> int:
+    """A tensor's address, an address, or 0 for None."""
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        return t or 0
+
+
 def kvq_plan_step(batch: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int,
                   seq_lens, new_lens, free_pages, free_count, page_table, seq_lens_out,
                   free_count_out, token_offsets, slots, positions, workspace, workspace_bytes: int,
                   stream=None, check: bool = True) -> int:
-    st = _lib.kvq_plan_step(batch, page_size, num_pages, max_pages, max_tokens, _ptr(seq_lens),
-                            _ptr(new_lens), _ptr(free_pages), _ptr(free_count), _ptr(page_table),
-                            _ptr(seq_lens_out), _ptr(free_count_out), _ptr(token_offsets),
-                            _ptr(slots), _ptr(positions), _ptr(workspace), int(workspace_bytes),
-                            _stream(stream))
+    st = _lib.kvq_packed_call(0, _PLAN.pack(
+        _i32(batch), _i32(page_size), _i32(num_pages), _i32(max_pages), _i32(max_tokens), _word(seq_lens), _word(new_lens),
+        _word(free_pages), _word(free_count), _word(page_table), _word(seq_lens_out), _word(free_count_out),
+        _word(token_offsets), _word(slots), _word(positions), _word(workspace), workspace_bytes, _stream(stream) or 0))
     if check:
         _check("kvq_plan_step", st)
     return st
@@ -307,11 +325,10 @@ def kvq_prompt_attn(desc: KvqCacheDesc, q, n_tokens: int, num_q_heads: int, k_co
                     token_offsets, batch: int, causal: bool, sm_scale: float, workspace,
                     workspace_bytes: int, out, out_type: int = KVQ_OUT_F32, stream=None,
                     check: bool = True) -> int:
-    st = _lib.kvq_prompt_attn(ctypes.byref(desc), _ptr(q), n_tokens, num_q_heads, _ptr(k_codes),
-                              _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(page_table),
-                              max_pages, _ptr(seq_lens), max_seq_len, _ptr(token_offsets), batch,
-                              int(causal), float(sm_scale), _ptr(workspace), int(workspace_bytes),
-                              _ptr(out), int(out_type), _stream(stream))
+    st = _lib.kvq_packed_call(1, _PROMPT.pack(
+        ctypes.addressof(desc), _word(q), _i32(n_tokens), _i32(num_q_heads), _word(k_codes), _word(k_scales), _word(v_codes),
+        _word(v_scales), _word(page_table), _i32(max_pages), _word(seq_lens), _i32(max_seq_len), _word(token_offsets),
+        _i32(batch), int(causal), sm_scale, _word(workspace), workspace_bytes, _word(out), out_type, _stream(stream) or 0))
     if check:
         _check("kvq_prompt_attn", st)
     return st
@@ -322,12 +339,11 @@ def kvq_prefix_attn(desc: KvqCacheDesc, q, batch: int, num_q_heads: int, k_codes
                     group_offsets, num_groups: int, page_table, max_pages: int, seq_lens,
                     max_seq_len: int, sm_scale: float, workspace, workspace_bytes: int, out,
                     out_type: int = KVQ_OUT_F32, stream=None, check: bool = True) -> int:
-    st = _lib.kvq_prefix_attn(ctypes.byref(desc), _ptr(q), batch, num_q_heads, _ptr(k_codes),
-                              _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(prefix_table),
-                              max_prefix_pages, _ptr(prefix_lens), max_prefix_len,
-                              _ptr(group_offsets), num_groups, _ptr(page_table), max_pages,
-                              _ptr(seq_lens), max_seq_len, float(sm_scale), _ptr(workspace),
-                              int(workspace_bytes), _ptr(out), int(out_type), _stream(stream))
+    st = _lib.kvq_packed_call(2, _PREFIX.pack(
+        ctypes.addressof(desc), _word(q), _i32(batch), _i32(num_q_heads), _word(k_codes), _word(k_scales), _word(v_codes),
+        _word(v_scales), _word(prefix_table), _i32(max_prefix_pages), _word(prefix_lens), _i32(max_prefix_len),
+        _word(group_offsets), _i32(num_groups), _word(page_table), _i32(max_pages), _word(seq_lens), _i32(max_seq_len),
+        sm_scale, _word(workspace), workspace_bytes, _word(out), out_type, _stream(stream) or 0))
     if check:
         _check("kvq_prefix_attn", st)
     return st

@@ -54,6 +54,7 @@ class QuantizedKVCache:
         self.desc = kb.make_desc(fmt, head_dim, num_kv_heads, page_size, num_pages,
                                  self.codebook, self.signs)
         self._ws = None
+        self._index = _cuda_index(self.device)
         self._ws_rows = None     # prompt and prefix attention
         self._rows_bytes = {}    # workspace bytes by request shape
 
@@ -113,19 +114,30 @@ class QuantizedKVCache:
         return out
 
     # ---------------------------------------------------------------- prompts, shared prefixes
-    def _rows_workspace(self, key, size_fn, args, stream):
+    def _rows_call(self, kind, size_fn, args, q, out, out_dtype, sm_scale, stream):
+        """Checks of q and out, the workspace, the output, the scale and the stream of a call."""
+        D = self.head_dim
+        if q.dim() != 3 or q.shape[2] != D:
+            raise ValueError(f"q must be [tokens, heads, {D}], not {tuple(q.shape)}")
+        _want("q", q, torch.float16, self._index)
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype, device=self.device)
+        elif out.shape != q.shape:
+            raise ValueError(f"out must have q's shape {tuple(q.shape)}, not {tuple(out.shape)}")
+        out_type = _OUT_TYPES.get(out.dtype)
+        if out_type is None:
+            raise ValueError(f"the output is float32 or float16, not {out.dtype}")
+        _want("out", out, out.dtype, self._index)
+        if stream is None:
+            stream = _raw_stream(self._index)
+        key = (kind,) + args
         nbytes = self._rows_bytes.get(key)
         if nbytes is None:
             nbytes = self._rows_bytes[key] = size_fn(self.desc, *args)
         if self._ws_rows is None or self._ws_rows.numel() < nbytes:
             self._ws_rows = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             kb.kvq_workspace_init(self._ws_rows, self._ws_rows.numel(), stream)
-        return self._ws_rows
-
-    def _rows_out(self, q, out, out_dtype):
-        if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype, device=self.device)
-        return out, _OUT_TYPES[out.dtype]
+        return out, out_type, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale, stream
 
     def prompt_attention(self, q: torch.Tensor, token_offsets: torch.Tensor, seq_lens: torch.Tensor,
                          max_seq_len: int, page_table: Optional[torch.Tensor] = None,
@@ -138,16 +150,24 @@ class QuantizedKVCache:
         packed; request b's are rows ``token_offsets[b]`` .. ``token_offsets[b + 1] - 1``
         and the last ones of its ``seq_lens[b]`` positions (write their K and V first).
         ``causal``: a token sees the positions up to its own.  Rows outside every request are
-        padding and keep what ``out`` holds there."""
-        n, Hq, D = q.shape
-        B = seq_lens.shape[0]
-        ws = self._rows_workspace(("prompt", n, Hq, B, max_seq_len), kb.kvq_prompt_workspace_size,
-                                  (n, Hq, B, max_seq_len), stream)
-        out, kind = self._rows_out(q, out, out_dtype)
-        kb.kvq_prompt_attn(self.desc, q, n, Hq, self.k_codes, self.k_scales, self.v_codes,
-                           self.v_scales, page_table, max_pages, seq_lens, max_seq_len,
-                           token_offsets, B, causal, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale,
-                           ws, ws.numel(), out, kind, stream)
+        padding and keep what ``out`` holds there.  Lengths, offsets and the table are int32
+        tensors on the cache's GPU."""
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.prompt_attention(q, token_offsets, seq_lens, max_seq_len, page_table, max_pages, causal,
+                                             sm_scale, out, out_dtype, stream)
+        B = seq_lens.numel()
+        _want("seq_lens", seq_lens, torch.int32, self._index)
+        _want("token_offsets", token_offsets, torch.int32, self._index, B + 1)
+        if page_table is not None:
+            _want("page_table", page_table, torch.int32, self._index, B * max_pages)
+        n, Hq = q.shape[0], q.shape[1]
+        out, out_type, sm_scale, stream = self._rows_call("prompt", kb.kvq_prompt_workspace_size, (n, Hq, B, max_seq_len),
+                                                          q, out, out_dtype, sm_scale, stream)
+        ws = self._ws_rows
+        kb.kvq_prompt_attn(self.desc, q, n, Hq, self.k_codes, self.k_scales, self.v_codes, self.v_scales, page_table,
+                           max_pages, seq_lens, max_seq_len, token_offsets, B, causal, sm_scale, ws, ws.numel(), out,
+                           out_type, stream)
         return out
 
     def prefix_attention(self, q: torch.Tensor, prefix_table: Optional[torch.Tensor],
@@ -161,27 +181,60 @@ class QuantizedKVCache:
         prefixes: group g (requests ``group_offsets[g]`` .. ``group_offsets[g + 1] - 1``; None:
         one group of all) attends to the ``prefix_lens[g]`` positions of row g of
         ``prefix_table`` and each request to its own ``seq_lens[b]`` positions as well.  The
-        prefix is read once per group, not once per request."""
-        B, Hq, D = q.shape
-        ng = prefix_lens.shape[0]
+        prefix is read once per group, not once per request.  Lengths, offsets and tables are
+        int32 tensors on the cache's GPU."""
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.prefix_attention(q, prefix_table, prefix_lens, max_prefix_len, seq_lens, max_seq_len,
+                                             page_table, max_pages, group_offsets, max_prefix_pages, sm_scale, out,
+                                             out_dtype, stream)
+        B, ng = q.shape[0], prefix_lens.numel()
         if max_prefix_pages is None:
             if prefix_table is None:
                 raise ValueError("max_prefix_pages is needed without a prefix_table")
-            max_prefix_pages = prefix_table.shape[1]
-        ws = self._rows_workspace(("prefix", B, Hq, ng, max_prefix_len, max_seq_len),
-                                  kb.kvq_prefix_workspace_size, (B, Hq, ng, max_prefix_len, max_seq_len),
-                                  stream)
-        out, kind = self._rows_out(q, out, out_dtype)
-        kb.kvq_prefix_attn(self.desc, q, B, Hq, self.k_codes, self.k_scales, self.v_codes,
-                           self.v_scales, prefix_table, max_prefix_pages, prefix_lens, max_prefix_len,
-                           group_offsets, ng, page_table, max_pages, seq_lens, max_seq_len,
-                           1.0 / math.sqrt(D) if sm_scale is None else sm_scale, ws, ws.numel(), out,
-                           kind, stream)
+            max_prefix_pages = prefix_table.shape[-1]
+        _want("prefix_lens", prefix_lens, torch.int32, self._index)
+        _want("seq_lens", seq_lens, torch.int32, self._index, B)
+        if prefix_table is not None:
+            _want("prefix_table", prefix_table, torch.int32, self._index, ng * max_prefix_pages)
+        if group_offsets is not None:
+            _want("group_offsets", group_offsets, torch.int32, self._index, ng + 1)
+        if page_table is not None:
+            _want("page_table", page_table, torch.int32, self._index, B * max_pages)
+        Hq = q.shape[1]
+        out, out_type, sm_scale, stream = self._rows_call(
+            "prefix", kb.kvq_prefix_workspace_size, (B, Hq, ng, max_prefix_len, max_seq_len), q, out, out_dtype, sm_scale,
+            stream)
+        ws = self._ws_rows
+        kb.kvq_prefix_attn(self.desc, q, B, Hq, self.k_codes, self.k_scales, self.v_codes, self.v_scales, prefix_table,
+                           max_prefix_pages, prefix_lens, max_prefix_len, group_offsets, ng, page_table, max_pages,
+                           seq_lens, max_seq_len, sm_scale, ws, ws.numel(), out, out_type, stream)
         return out
 
     def device_flags(self) -> int:
         flags = 0 if self._ws is None else kb.kvq_read_device_flags(self._ws)
         return flags if self._ws_rows is None else flags | kb.kvq_read_device_flags(self._ws_rows)
+
+
+def _want(name: str, t: torch.Tensor, dtype: torch.dtype, index: int, numel: Optional[int] = None) -> None:
+    """The kernels read plain contiguous memory of the cache's GPU: refuse anything else."""
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index or (
+            numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{index}"
+                         + (f" of {numel} elements" if numel is not None else "")
+                         + f", not {t.dtype} {tuple(t.shape)} on {t.device}"
+                         + ("" if t.is_contiguous() else " (not contiguous)"))
+
+
+def _cuda_index(device: torch.device) -> int:
+    """The GPU of a device ("cuda" is the current one); -1 without one."""
+    if device.type != "cuda":
+        return -1
+    return torch.cuda.current_device() if device.index is None else device.index
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 _OUT_TYPES = {torch.float32: kb.KVQ_OUT_F32, torch.float16: kb.KVQ_OUT_F16}
@@ -200,6 +253,7 @@ class PagePlanner:
         self.batch, self.page_size, self.num_pages = batch, page_size, num_pages
         self.max_pages, self.max_tokens = max_pages, max_tokens
         self.device = torch.device(device)
+        self._index = _cuda_index(self.device)
         ints = lambda n: torch.zeros(n, dtype=torch.int32, device=self.device)  # noqa: E731
         self.seq_lens, self.token_offsets, self.free_count = ints(batch), ints(batch + 1), ints(1)
         self.slots, self.positions = ints(max_tokens), ints(max_tokens)
@@ -207,11 +261,24 @@ class PagePlanner:
 
     def step(self, new_lens: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
              free_pages: torch.Tensor, free_count: torch.Tensor, stream=None) -> None:
-        """Plan one step: ``new_lens[b]`` tokens to append per request, -1 where it ends."""
+        """Plan one step: ``new_lens[b]`` tokens to append per request, -1 where it ends.  All
+        are int32 tensors on the planner's GPU: ``page_table`` [batch, max_pages],
+        ``free_pages`` [num_pages]."""
+        i = self._index
+        if torch.cuda.current_device() != i:
+            with torch.cuda.device(i):
+                return self.step(new_lens, page_table, seq_lens, free_pages, free_count, stream)
+        _want("new_lens", new_lens, torch.int32, i, self.batch)
+        _want("page_table", page_table, torch.int32, i, self.batch * self.max_pages)
+        _want("seq_lens", seq_lens, torch.int32, i, self.batch)
+        _want("free_pages", free_pages, torch.int32, i)
+        if free_pages.numel() < self.num_pages:
+            raise ValueError(f"free_pages must hold num_pages = {self.num_pages} entries, not {free_pages.numel()}")
+        _want("free_count", free_count, torch.int32, i, 1)
         kb.kvq_plan_step(self.batch, self.page_size, self.num_pages, self.max_pages, self.max_tokens,
                          seq_lens, new_lens, free_pages, free_count, page_table, self.seq_lens,
                          self.free_count, self.token_offsets, self.slots, self.positions, self._ws,
-                         256, stream)
+                         256, _raw_stream(i) if stream is None else stream)
 
     def device_flags(self) -> int:
         """KVQ_FLAG_* bits of the steps so far (a flagged step changed nothing)."""

@@ -1,6 +1,7 @@
 // C-ABI entry points of the serving operators: the page plan of a step, prompt attention and
 // shared-prefix decode.  Argument validation, then the launches; nothing is launched on an error.
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -240,6 +241,36 @@ int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, in
   st = launch_rows(r, own, s);
   if (st != KVQ_OK) return st;
   return launch_rows_merge(r, own, out, out_type == KVQ_OUT_F16, s);
+}
+
+// The three calls above from one block of 64-bit words, in their arguments' order (pointers and
+// integers as they are, a float as a double's bits): for bindings whose cost per argument counts.
+int kvq_packed_call(int32_t which, const int64_t* w) {
+  if (!w) return KVQ_ERR_INVALID_ARG;
+  auto ptr = [&](int i) { return reinterpret_cast<void*>(static_cast<uintptr_t>(w[i])); };
+  auto ints = [&](int i) { return static_cast<int32_t*>(ptr(i)); };
+  auto num = [&](int i) { return static_cast<int32_t>(w[i]); };
+  auto real = [&](int i) {
+    double d;
+    memcpy(&d, w + i, sizeof d);
+    return static_cast<float>(d);
+  };
+  const kvq_cache_desc* desc = static_cast<const kvq_cache_desc*>(ptr(0));
+  switch (which) {
+    case 0:
+      return kvq_plan_step(num(0), num(1), num(2), num(3), num(4), ints(5), ints(6), ints(7), ints(8), ints(9), ints(10),
+                           ints(11), ints(12), ints(13), ints(14), ptr(15), (size_t)w[16], ptr(17));
+    case 1:
+      return kvq_prompt_attn(desc, ptr(1), num(2), num(3), ptr(4), ptr(5), ptr(6), ptr(7), ints(8), num(9), ints(10),
+                             num(11), ints(12), num(13), num(14), real(15), ptr(16), (size_t)w[17], ptr(18), num(19),
+                             ptr(20));
+    case 2:
+      return kvq_prefix_attn(desc, ptr(1), num(2), num(3), ptr(4), ptr(5), ptr(6), ptr(7), ints(8), num(9), ints(10),
+                             num(11), ints(12), num(13), ints(14), num(15), ints(16), num(17), real(18), ptr(19),
+                             (size_t)w[20], ptr(21), num(22), ptr(23));
+    default:
+      return KVQ_ERR_INVALID_ARG;
+  }
 }
 
 }  // extern "C"
