@@ -64,7 +64,9 @@ struct Shared {
   uint64_t s_full[2], p_half[2], p_full[2];  // a stream's scores; first half, rest of its weights
   uint64_t q_full;                                        // query rows
   uint64_t done;                                          // every MMA completed
-  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];         // staged codes and scales of half tiles
+  // Staged codes and scales of half tiles.  A stage is filled for either half's warps in turn, and
+  // a wait by parity must not meet a phase that is not its waiter's: one barrier per half.
+  uint64_t raw_full[2][kMaxRaw], raw_empty[kMaxRaw];
   uint32_t tmem;
   int unit[6];  // group, first token row, rows, positions, new tokens, valid
   float merge_m[128], merge_l[128];
@@ -137,12 +139,10 @@ __device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8
   constexpr int kTasks = kTile * kChunks / 128;  // per thread
   static_assert(kTasks >= 1, "a chunk for every thread");
   const uint8_t* scales = raw + kTile * C::CROW;
-#pragma unroll
-  for (int i = 0; i < kTasks; ++i) {
-    // Row and code chunk: dealt so that eight neighbours read eight different bank groups of
-    // the staged codes and write eight different ones of the swizzled tile (whose two column
-    // groups coincide modulo the banks): rows next to each other take opposite row halves.
-    int row, j;
+  // Row and code chunk of task i: dealt so that eight neighbours read eight different bank
+  // groups of the staged codes and write eight different ones of the swizzled tile (whose two
+  // column groups coincide modulo the banks): rows next to each other take opposite row halves.
+  auto place = [&](int i, int& row, int& j) {
     if constexpr (kChunks == 8) {
       row = 2 * (tid >> 3) + (tid >> 2 & 1) + 32 * (i >> 1);
       j = (tid & 3) + 4 * ((tid >> 2 & 1) ^ (i & 1));
@@ -153,25 +153,37 @@ __device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8
       row = (i * 128 + tid) / kChunks;
       j = tid % kChunks;
     }
-    uint4 u = *reinterpret_cast<const uint4*>(raw + row * C::CROW + j * 16);
+  };
+  // every load first: the stores below might alias them for all the compiler knows
+  uint4 u[kTasks];
+  __half2 d[kTasks][C::kNv ? 2 : 1];
+#pragma unroll
+  for (int i = 0; i < kTasks; ++i) {
+    int row, j;
+    place(i, row, j);
+    u[i] = *reinterpret_cast<const uint4*>(raw + row * C::CROW + j * 16);
     const bool live = row < n_valid;
     const uint8_t* sp = scales + row * C::SROW;
-    __half2 d0, d1;
     if constexpr (C::kNv) {
       const uint32_t e = lds16(sp + 2 * j);
       const float g = *reinterpret_cast<const float*>(sp + D / 16);
-      d0 = __float2half2_rn(live ? e4m3_float(e & 0xffu) * g : 0.f);
-      d1 = __float2half2_rn(live ? e4m3_float(e >> 8) * g : 0.f);
+      d[i][0] = __float2half2_rn(live ? e4m3_float(e & 0xffu) * g : 0.f);
+      d[i][1] = __float2half2_rn(live ? e4m3_float(e >> 8) * g : 0.f);
     } else {
       const uint32_t b = lds16(sp + (C::kQ8 ? j >> 1 : C::kQ4 ? j : 0) * 2);
-      d0 = d1 = __half2half2(__ushort_as_half((unsigned short)(live ? b : 0u)));
+      d[i][0] = __half2half2(__ushort_as_half((unsigned short)(live ? b : 0u)));
     }
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  }
+#pragma unroll
+  for (int i = 0; i < kTasks; ++i) {
+    int row, j;
+    place(i, row, j);
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
     constexpr int kOut = C::kQ8 ? 2 : 4;  // 16-byte chunks of eight values
 #pragma unroll
     for (int c = 0; c < kOut; ++c) {
-      const uint4 v = C::kQ8 ? dequant8<FMT, D>(w[2 * c & 3], w[(2 * c + 1) & 3], d0, lut)
-                             : dequant8<FMT, D>(w[c], 0u, c < 2 ? d0 : d1, lut);
+      const uint4 v = C::kQ8 ? dequant8<FMT, D>(w[2 * c & 3], w[(2 * c + 1) & 3], d[i][0], lut)
+                             : dequant8<FMT, D>(w[c], 0u, d[i][C::kNv ? c >> 1 : 0], lut);
       *reinterpret_cast<uint4*>(tile + tile_offset(row0 + row, kOut * j + c)) = v;
     }
   }
@@ -282,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       bar_init(&sh.q_full, kSoftmaxWarps);
       bar_init(&sh.done, 1);
       for (int i = 0; i < S::kStages; ++i) {
-        bar_init(&sh.raw_full[i], 1);
+        bar_init(&sh.raw_full[0][i], 1);
+        bar_init(&sh.raw_full[1][i], 1);
         bar_init(&sh.raw_empty[i], kFillWarps / 2);
       }
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -426,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
         };
         int krow = row_of(lane), vrow = krow;  // of blocks 32 i + lane, i the current window
         int h = 0;
+        uint32_t phase[2] = {0u, 0u}, last = 0u;  // per stage: each half's next parity, the half that used it last
         for (int t = -2; ok && t < tiles; ++t) {
           for (int which = 0; ok && which < 2; ++which) {
             const int tt = which ? t + 2 : t;
@@ -440,21 +454,26 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
               if (!ok) break;
               if (lane == 0) {
                 uint8_t* dst = smem + S::kRaw + st * S::kRawBytes;
+                uint64_t* full = &sh.raw_full[half][st];
                 if (row >= 0) {
-                  bar_expect(&sh.raw_full[st], S::kRawBytes);
-                  bulk_load(dst, (which ? kc : vc) + (int64_t)row * C::CROW, S::kRawCodes, &sh.raw_full[st]);
-                  bulk_load(dst + S::kRawCodes, (which ? ks : vs) + (int64_t)row * C::SROW, S::kRawScales,
-                            &sh.raw_full[st]);
+                  bar_expect(full, S::kRawBytes);
+                  bulk_load(dst, (which ? kc : vc) + (int64_t)row * C::CROW, S::kRawCodes, full);
+                  bulk_load(dst + S::kRawCodes, (which ? ks : vs) + (int64_t)row * C::SROW, S::kRawScales, full);
                 } else {
-                  bar_arrive(&sh.raw_full[st]);  // whatever the stage holds: the call is flagged
+                  bar_arrive(full);  // whatever the stage holds: the call is flagged
                 }
               }
+              phase[half] ^= 1u << st;
+              last = (last & ~(1u << st)) | (uint32_t)half << st;
               ++h;
             }
           }
         }
         // no copy may land after the block has gone (each was waited for, unless a wait gave up)
-        for (int i = max(0, h - S::kStages); i < h; ++i) (void)bar_wait(&sh.raw_full[i % S::kStages], i / S::kStages & 1);
+        for (int st = 0; st < min(h, S::kStages); ++st) {
+          const int half = last >> st & 1;
+          (void)bar_wait(&sh.raw_full[half][st], (phase[half] >> st & 1) ^ 1);
+        }
       }
       __syncwarp();
     } else if (warp >= kSoftmaxWarps) {
@@ -481,22 +500,27 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       }
       // four warps per half tile; a half past the last position is filled with zeros
       const int half = ft >> 7;
-      int staged = 0;  // half tiles staged before this tile's
+      int staged = 0;        // half tiles staged before this tile's
+      uint32_t phase = 0u;   // next parity of this half's barrier of each stage
       auto put = [&](int t, uint8_t* slots, uint64_t* full, uint64_t* empty) {
         const int p = begin + t * kKvTile;
         const int n_half = p + kTile < end ? 2 : 1;
         ok = t < 2 || bar_wait(&empty[t & 1], (t >> 1 & 1) ^ 1);
         if (!ok) return;
         const int h = staged + half;
-        const uint8_t* raw = smem + S::kRaw + h % S::kStages * S::kRawBytes;
-        if (half < n_half) ok = bar_wait(&sh.raw_full[h % S::kStages], h / S::kStages & 1);
-        if (!ok) return;
+        const int st = h % S::kStages;
+        const uint8_t* raw = smem + S::kRaw + st * S::kRawBytes;
+        if (half < n_half) {
+          ok = bar_wait(&sh.raw_full[half][st], phase >> st & 1);
+          if (!ok) return;
+          phase ^= 1u << st;
+        }
         fill_half<FMT, D>(raw, slots + (t & 1) * S::kTileBytes, half * kTile, end - p - half * kTile, ft & 127, lut);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
           bar_arrive(&full[t & 1]);
-          if (half < n_half) bar_arrive(&sh.raw_empty[h % S::kStages]);
+          if (half < n_half) bar_arrive(&sh.raw_empty[st]);
         }
         staged += n_half;
       };
@@ -600,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       const int steps = shared_tiles ? tiles : (tiles - s + 1) / 2;
       const uint32_t ts = at + s * 128, to = at + 256 + s * D;  // scores, accumulator
       const uint64_t scale2 = pack_f2(scale, scale);
+      const bool idle = (shared_tiles ? s * 128 : 0) + (warp & 3) * 32 >= rows;  // no row of this warp exists
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < steps; ++i) {
         const int t = shared_tiles ? i : 2 * i + s;
@@ -607,6 +632,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
         ok = bar_wait(&sh.s_full[s], i & 1);
         if (!ok) break;
         tc_fence_after();
+        if (idle) {  // the MMA reads whatever these rows hold: rows do not mix
+          if (lane == 0) {
+            bar_arrive(&sh.p_half[s]);
+            bar_arrive(&sh.p_full[s]);
+          }
+          continue;
+        }
         const bool mask = __any_sync(0xffffffffu, lim < kKvTile);
         float v[kKvTile];
 #pragma unroll
