@@ -58,7 +58,7 @@ constexpr uint32_t kTmemColumns = 512;
 template <int FMT>
 constexpr float kUnhalve = FMT == KVQ_FMT_Q8_0 || FMT == KVQ_FMT_NVFP4 ? 2.f : 1.f;
 
-constexpr int kMaxRaw = 8;
+constexpr int kMaxRaw = 10;
 struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // K / V tile slots
   uint64_t s_full[2], p_half[2], p_full[2];  // a stream's scores; first half, rest of its weights
@@ -68,7 +68,7 @@ struct Shared {
   // a wait by parity must not meet a phase that is not its waiter's: one barrier per half.
   uint64_t raw_full[2][kMaxRaw], raw_empty[kMaxRaw];
   uint32_t tmem;
-  int unit[6];  // group, first token row, rows, positions, new tokens, valid
+  int unit[9];  // see find_unit
   float merge_m[128], merge_l[128];
 };
 
@@ -84,6 +84,8 @@ struct Smem {
   static constexpr int kRawBytes = kRawCodes + kRawScales;
   static constexpr int kRoom = 227 * 1024 - 1024 - (int)sizeof(Shared) - kRaw;
   static constexpr int kStages = kRoom / kRawBytes < kMaxRaw ? kRoom / kRawBytes : kMaxRaw;
+  // a unit of one row tile leaves the second one's space to more stages
+  static constexpr int kExtra = kTileBytes / kRawBytes < kMaxRaw - kStages ? kTileBytes / kRawBytes : kMaxRaw - kStages;
   static constexpr int kBars = kRaw + kStages * kRawBytes;
   static constexpr int kBytes = kBars + (int)sizeof(Shared) + 1024;  // slack: 1024-byte alignment
   static_assert(256 * (D * 4 + 16) <= kRaw && 128 * (D * 4 + 16) <= kV, "room for the results");
@@ -190,30 +192,70 @@ __device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8
 }
 
 // ------------------------------------------------------------------ unit lookup
-// Row tile `t` (over all groups): its group and first row.  One warp; the lanes take
-// consecutive ranges of groups.
+// Block `t`'s unit: group, first row, rows, positions, first token, tokens (0: no such unit), KV
+// head, split, positions per split.  One warp; the lanes take consecutive ranges of groups.  The
+// chunk balances groups of unequal lengths (up to 32 groups): about the shortest multiple of kKvTile
+// for which the units (row tile, KV head, split) number at most a.ctas.
 __device__ __forceinline__ void find_unit(const RowsArgs& a, int t, int lane, int* unit) {
-  const int per = (a.num_groups + 31) / 32;
+  const int per = (a.num_groups + 31) / 32, hkv = a.desc.num_kv_heads;
   const int g0 = min(lane * per, a.num_groups), g1 = min(g0 + per, a.num_groups);
-  const int len0 = g0 < g1 ? a.lens[g0] : 0;  // in flight with the offsets
-  auto tokens = [&](int g, int& first) {
-    if (!a.offsets) {
-      first = 0;
-      return a.n_tokens;
+  auto group = [&](int g, int& first, int& len) {  // tokens
+    first = a.offsets ? a.offsets[g] : 0;
+    const int end = a.offsets ? a.offsets[g + 1] : a.n_tokens;
+    len = a.lens[g];
+    if (len < 0 || len > a.max_len || len > (int64_t)a.max_pages * a.desc.page_size) {
+      set_flag(a.flags, KVQ_FLAG_BAD_SEQLEN);
+      len = 0;
     }
-    first = a.offsets[g];
-    const int end = a.offsets[g + 1];
     if (first < 0 || end < first || end > a.n_tokens) {
       set_flag(a.flags, KVQ_FLAG_BAD_SEQLEN);
       return 0;
     }
     return end - first;
   };
-  int mine = 0, first = 0, n0 = 0;
-  for (int g = g0; g < g1; ++g) {
-    n0 = tokens(g, first);
-    mine += (n0 * a.group + kRowTile - 1) / kRowTile;
+  auto tiles_of = [&](int n) { return (n * a.group + kRowTile - 1) / kRowTile; };
+  // splits of a group; with direct output a unit without positions still writes its zeros
+  auto splits_of = [&](int len, int chunk) { return max((len + chunk - 1) / chunk, a.out ? 1 : 0); };
+  int first0 = 0, len0 = 0, n0 = 0;  // of group g0 (the only one of this lane when per is 1)
+  if (g0 < g1) n0 = group(g0, first0, len0);
+  auto units = [&](int chunk) {  // of this lane's groups
+    int u = 0;
+    for (int g = g0; g < g1; ++g) {
+      int first = first0, len = len0;
+      const int n = g == g0 ? n0 : group(g, first, len);
+      u += tiles_of(n) * splits_of(len, chunk) * hkv;
+    }
+    return u;
+  };
+  int chunk = a.min_chunk;
+  if (a.splits > 1) {
+    // In tiles of kKvTile.  32 candidates at a time, one per lane, between the even share of all
+    // the work and the longest group; then again around the best.  (The candidates' units by
+    // approximate reciprocals: a unit more or less than a.ctas only costs balance.)
+    const int t0 = tiles_of(n0) * hkv, l0 = (len0 + kKvTile - 1) / kKvTile;
+    int lo, hi = max(a.min_chunk / kKvTile, 1);
+    lo = hi;
+    if (per == 1) {
+      const float share = (float)__reduce_add_sync(0xffffffffu, (unsigned)(t0 * l0)) / (float)a.ctas;
+      lo = max(lo, (int)ceilf(share));
+      hi = max(lo, (int)__reduce_max_sync(0xffffffffu, (unsigned)l0));
+      for (int pass = 0; pass < 2 && lo < hi; ++pass) {
+        const int step = (hi - lo + 31) >> 5;
+        const int c = min(lo + lane * step, hi);
+        const float r = __frcp_rn((float)c);
+        int u = 0;
+        for (int g = 0; g < a.num_groups; ++g)
+          u += __shfl_sync(0xffffffffu, t0, g) * (int)ceilf((float)__shfl_sync(0xffffffffu, l0, g) * r - 1e-3f);
+        const uint32_t fits = __ballot_sync(0xffffffffu, u <= a.ctas);
+        const int k = fits ? __ffs(fits) - 1 : 32;
+        hi = min(lo + k * step, hi);
+        lo = k > 0 ? min(lo + (k - 1) * step + 1, hi) : lo;
+      }
+    }
+    chunk = hi * kKvTile;
+    if (t == 0 && lane == 0) *a.chunk_out = chunk;
   }
+  const int mine = units(chunk);
   int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -226,25 +268,26 @@ __device__ __forceinline__ void find_unit(const RowsArgs& a, int t, int lane, in
   if (t >= before && t < before + mine) {
     int k = t - before;
     for (int g = g0; g < g1; ++g) {
-      const int n = per == 1 ? n0 : tokens(g, first);
-      const int tiles = (n * a.group + kRowTile - 1) / kRowTile;
-      if (k < tiles) {
-        // the last rows of a causal group see the most positions: they start first
-        const int tile = a.causal ? tiles - 1 - k : k;
-        int len = g == g0 ? len0 : a.lens[g];
-        if (len < 0 || len > a.max_len || len > (int64_t)a.max_pages * a.desc.page_size) {
-          set_flag(a.flags, KVQ_FLAG_BAD_SEQLEN);
-          len = 0;
-        }
+      int first = first0, len = len0;
+      const int n = g == g0 ? n0 : group(g, first, len);
+      const int tiles = tiles_of(n), splits = splits_of(len, chunk);
+      if (k < tiles * splits * hkv) {
+        // split fastest, then KV head; the last rows of a causal group see the most positions:
+        // they start first
+        const int row_tile = k / splits / hkv;
+        const int tile = a.causal ? tiles - 1 - row_tile : row_tile;
         unit[0] = g;
         unit[1] = tile * kRowTile;
         unit[2] = min(n * a.group - tile * kRowTile, kRowTile);
         unit[3] = len;
         unit[4] = first;
         unit[5] = n;
+        unit[6] = k / splits % hkv;
+        unit[7] = k % splits;
+        unit[8] = chunk;
         break;
       }
-      k -= tiles;
+      k -= tiles * splits * hkv;
     }
   }
   __syncwarp();
@@ -273,12 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
     }
     return;
   }
-  // block: split fastest, then KV head, then row tile
-  const int split = blockIdx.x % a.splits;
-  const int kvh = blockIdx.x / a.splits % hkv;
-  const int rt = blockIdx.x / a.splits / hkv;
 
-  if (warp == 0) find_unit(a, rt, lane, sh.unit);
+  if (warp == 0) find_unit(a, blockIdx.x, lane, sh.unit);
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem, kTmemColumns);
     if (lane == 0) {
@@ -293,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       }
       bar_init(&sh.q_full, kSoftmaxWarps);
       bar_init(&sh.done, 1);
-      for (int i = 0; i < S::kStages; ++i) {
+      for (int i = 0; i < S::kStages + S::kExtra; ++i) {
         bar_init(&sh.raw_full[0][i], 1);
         bar_init(&sh.raw_full[1][i], 1);
         bar_init(&sh.raw_empty[i], kFillWarps / 2);
@@ -305,13 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
   __syncthreads();
   tc_fence_after();
   const int g = sh.unit[0], row0 = sh.unit[1], rows = sh.unit[2], len = sh.unit[3], tok0 = sh.unit[4], n = sh.unit[5];
+  const int kvh = sh.unit[6], split = sh.unit[7], chunk = sh.unit[8];
   // positions of this split that any row of the unit sees
   const int last = n > 0 ? row_limit(len, n, (row0 + rows - 1) / G, a.causal) : 0;
-  const int begin = split * a.chunk;
-  const int end = min(min(last, len), begin + a.chunk);
+  const int begin = n > 0 ? split * chunk : 0;
+  const int end = n > 0 ? min(min(last, len), begin + chunk) : 0;
   const int tiles = end > begin ? (end - begin + kKvTile - 1) / kKvTile : 0;
   const bool shared_tiles = rows > 128;  // both streams take every tile; else every other one
   const bool live = n > 0 && (tiles > 0 || a.out != nullptr);
+  const int stages = shared_tiles ? S::kStages : S::kStages + S::kExtra;
+  auto stage_at = [&](int st) {
+    return smem + (st < S::kStages ? S::kRaw + st * S::kRawBytes : S::kQ + S::kTileBytes + (st - S::kStages) * S::kRawBytes);
+  };
 
   const uint32_t tmem = sh.tmem;
   bool ok = true;
@@ -331,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
         const uint64_t kd = mma_desc(smem_u32(smem + S::kK), 16, 1024);
         const uint64_t vd = mma_desc(smem_u32(smem + S::kV), 16384, 1024);
         auto qk = [&](int s, int slot) {
-          const uint64_t qa = qd + s * kTileUnits, ka = kd + slot * kTileUnits;
+          const uint64_t qa = qd + (shared_tiles ? s : 0) * kTileUnits, ka = kd + slot * kTileUnits;
           const uint32_t dst = tmem + s * 128;
           if (leader) {
 #pragma unroll
@@ -438,8 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
           return (page * hkv + kvh) * ps + (p - pg * ps);
         };
         int krow = row_of(lane), vrow = krow;  // of blocks 32 i + lane, i the current window
-        int h = 0;
-        uint32_t phase[2] = {0u, 0u}, last = 0u;  // per stage: each half's next parity, the half that used it last
+        int h = 0, st = 0;      // half tiles so far, the stage of the next
+        uint32_t round = 0u;    // parity of the ring's passes
+        uint32_t phase0 = 0u, phase1 = 0u, last = 0u;  // per stage: each half's next parity, the half that used it last
         for (int t = -2; ok && t < tiles; ++t) {
           for (int which = 0; ok && which < 2; ++which) {
             const int tt = which ? t + 2 : t;
@@ -447,13 +492,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
             for (int half = 0; ok && half < 2; ++half) {
               const int hb = 2 * tt + half;
               if (begin + hb * kTile >= end) break;
-              if ((hb & 31) == 0 && hb > 0) (which ? krow : vrow) = row_of(hb + lane);
+              if ((hb & 31) == 0 && hb > 0) {
+                const int next = row_of(hb + lane);
+                if (which) krow = next; else vrow = next;
+              }
               const int row = __shfl_sync(0xffffffffu, which ? krow : vrow, hb & 31);
-              const int st = h % S::kStages;
-              ok = h < S::kStages || bar_wait(&sh.raw_empty[st], (h / S::kStages & 1) ^ 1);
+              ok = h < stages || bar_wait(&sh.raw_empty[st], round ^ 1);
               if (!ok) break;
               if (lane == 0) {
-                uint8_t* dst = smem + S::kRaw + st * S::kRawBytes;
+                uint8_t* dst = stage_at(st);
                 uint64_t* full = &sh.raw_full[half][st];
                 if (row >= 0) {
                   bar_expect(full, S::kRawBytes);
@@ -463,16 +510,20 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
                   bar_arrive(full);  // whatever the stage holds: the call is flagged
                 }
               }
-              phase[half] ^= 1u << st;
+              if (half) phase1 ^= 1u << st; else phase0 ^= 1u << st;
               last = (last & ~(1u << st)) | (uint32_t)half << st;
               ++h;
+              if (++st == stages) {
+                st = 0;
+                round ^= 1u;
+              }
             }
           }
         }
         // no copy may land after the block has gone (each was waited for, unless a wait gave up)
-        for (int st = 0; st < min(h, S::kStages); ++st) {
+        for (st = 0; st < min(h, stages); ++st) {
           const int half = last >> st & 1;
-          (void)bar_wait(&sh.raw_full[half][st], (phase[half] >> st & 1) ^ 1);
+          (void)bar_wait(&sh.raw_full[half][st], ((half ? phase1 : phase0) >> st & 1) ^ 1);
         }
       }
       __syncwarp();
@@ -500,16 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       }
       // four warps per half tile; a half past the last position is filled with zeros
       const int half = ft >> 7;
-      int staged = 0;        // half tiles staged before this tile's
+      int next_stage = 0;    // of this tile's first half
       uint32_t phase = 0u;   // next parity of this half's barrier of each stage
       auto put = [&](int t, uint8_t* slots, uint64_t* full, uint64_t* empty) {
         const int p = begin + t * kKvTile;
         const int n_half = p + kTile < end ? 2 : 1;
         ok = t < 2 || bar_wait(&empty[t & 1], (t >> 1 & 1) ^ 1);
         if (!ok) return;
-        const int h = staged + half;
-        const int st = h % S::kStages;
-        const uint8_t* raw = smem + S::kRaw + st * S::kRawBytes;
+        const int st = next_stage + half < stages ? next_stage + half : 0;
+        const uint8_t* raw = stage_at(st);
         if (half < n_half) {
           ok = bar_wait(&sh.raw_full[half][st], phase >> st & 1);
           if (!ok) return;
@@ -522,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
           bar_arrive(&full[t & 1]);
           if (half < n_half) bar_arrive(&sh.raw_empty[st]);
         }
-        staged += n_half;
+        next_stage += n_half;
+        if (next_stage >= stages) next_stage -= stages;
       };
       for (int t = -2; ok && t < tiles; ++t) {
         if (t >= 0) put(t, smem + S::kV, sh.v_full, sh.v_empty);
@@ -532,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       // ---------------------------------------------------------------- softmax
       regs_grow<kSoftmaxRegs>();
       // query rows, fp16, K-major, 128-byte swizzle; rows past the unit's are zero.  The loads
-      // of several rows are in flight together.  A unit of one row tile fills both.
+      // of several rows are in flight together.  A unit of one row tile has one for both streams.
       {
         const __half* q = static_cast<const __half*>(a.q) + (int64_t)kvh * G * D;
         const bool zero = a.sm_scale == 0.f;
@@ -560,7 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
               v[i].x ^= flip; v[i].y ^= flip; v[i].z ^= flip; v[i].w ^= flip;
               uint8_t* dst = smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, c);
               *reinterpret_cast<uint4*>(dst) = v[i];
-              if (!shared_tiles) *reinterpret_cast<uint4*>(dst + S::kTileBytes) = v[i];
             }
           }
         } else {
@@ -607,7 +657,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
               const uint4 h = make_uint4(pack_h2(z[0], z[1]), pack_h2(z[2], z[3]), pack_h2(z[4], z[5]), pack_h2(z[6], z[7]));
               uint8_t* dst = smem + S::kQ + (r >> 7) * S::kTileBytes + tile_offset(r & 127, part * 2 + c);
               *reinterpret_cast<uint4*>(dst) = h;
-              if (!shared_tiles) *reinterpret_cast<uint4*>(dst + S::kTileBytes) = h;
             }
           }
         }
@@ -836,19 +885,23 @@ int launch_t(const RowsArgs& a, const OwnArgs& own, cudaStream_t stream) {
 
 }  // namespace
 
-// One CTA per SM: a unit is cut along its positions until the units fill the device, in
-// pieces of at least two tiles (one per stream when the rows fit one row tile).
+// One CTA per SM: units are cut along their positions until they fill the device, in pieces of
+// at least two tiles (one per stream when the rows fit one row tile).  Groups of unequal
+// lengths may be cut into up to four times the splits that equal ones would need; the device
+// chooses among them (find_unit).
 RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, int max_len, int ctas) {
   RowsPlan p;
   const int64_t rows = (int64_t)n_tokens * group;
   p.row_tiles = (int)((rows + (int64_t)num_groups * (kRowTile - 1)) / kRowTile);
   const int64_t units = std::max<int64_t>(1, (int64_t)p.row_tiles * num_kv_heads);
-  const int64_t want = std::max<int64_t>(1, ctas / units);
+  int64_t want = std::max<int64_t>(1, ctas / units);
+  if (num_groups > 1 && num_groups <= 32 && want > 1) want = std::min<int64_t>(4 * want, std::max(1, ctas / num_kv_heads));
   const int64_t len = std::max(max_len, 1);
   int64_t chunk = (len + want - 1) / want;
   chunk = std::max<int64_t>((chunk + kKvTile - 1) / kKvTile * kKvTile, 2 * kKvTile);
-  p.chunk = (int)std::min<int64_t>(chunk, 0x7fffff00);
+  p.min_chunk = (int)std::min<int64_t>(chunk, 0x7fffff00);
   p.splits = (int)((len + chunk - 1) / chunk);
+  p.ctas = ctas;
   return p;
 }
 

@@ -29,8 +29,13 @@ struct RowsArgs {
   int num_groups;
   int causal;              // token i of n sees the positions < lens - n + i + 1; else all
   float sm_scale;
-  int splits, chunk;       // each unit's positions are cut at multiples of chunk (of kKvTile)
+  int splits;              // splits of a unit at the most
+  int min_chunk;           // each unit's positions are cut at multiples of a chunk chosen on the
+                           // device (of kKvTile, at least this): the shortest whose units all run at
+                           // once on `ctas` CTAs.  One split: max_len.
+  int ctas;
   int row_tiles;           // row tiles of all groups at the most
+  int32_t* chunk_out;      // the chunk, for the merge
   // out != null: one split, the rows are normalized and written here; otherwise partials:
   float* part_o;           // [n_tokens][num_q_heads][splits][head_dim], unnormalized
   float* part_m;           // [n_tokens][num_q_heads][splits] running maximum, log2 units
@@ -55,7 +60,7 @@ struct OwnArgs {
 
 // The split of a request: row tiles, splits and positions per split.
 struct RowsPlan {
-  int row_tiles, splits, chunk;
+  int row_tiles, splits, min_chunk, ctas;
 };
 RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, int max_len, int ctas);
 size_t rows_partial_bytes(int n_tokens, int num_q_heads, int head_dim, int splits);

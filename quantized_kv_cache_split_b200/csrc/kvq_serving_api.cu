@@ -13,6 +13,7 @@ namespace kvq {
 namespace {
 
 constexpr int kMaxLen = 1 << 30;
+constexpr int kChunkWord = 40;  // 32-bit word of the workspace header that holds the rows launch's chunk
 
 // What kvq_prompt_attn and kvq_prefix_attn ask of a request besides its pointers.
 int check_rows(const kvq_cache_desc* desc, int64_t n_tokens, int num_q_heads, int groups, int max_len) {
@@ -162,7 +163,9 @@ int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
   r.causal = causal;
   r.sm_scale = sm_scale;
   r.splits = p.splits;
-  r.chunk = p.chunk;
+  r.min_chunk = p.min_chunk;
+  r.ctas = p.ctas;
+  r.chunk_out = static_cast<int32_t*>(workspace) + kChunkWord;
   r.row_tiles = p.row_tiles;
   r.flags = static_cast<uint32_t*>(workspace);
   if (merge) set_partials(&r, static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
@@ -220,7 +223,9 @@ int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, in
   r.causal = 0;
   r.sm_scale = sm_scale;
   r.splits = p.rows.splits;
-  r.chunk = p.rows.chunk;
+  r.min_chunk = p.rows.min_chunk;
+  r.ctas = p.rows.ctas;
+  r.chunk_out = static_cast<int32_t*>(workspace) + kChunkWord;
   r.row_tiles = max_prefix_len > 0 ? p.rows.row_tiles : 0;
   r.flags = reinterpret_cast<uint32_t*>(ws);
   set_partials(&r, ws + kWorkspaceHeader);

@@ -181,6 +181,27 @@ def test_prompt_long_context_splits(fmt, half):
     run_prompt(pool, 8, [5000, 1500], [3, 9], half=half, max_extra=1000)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_few_rows(fmt, D):
+    # requests of a token or a few (at most 16 rows), beside one with more and one without any
+    pool = Pool(fmt, D, 2, 64, 60, seed=20)
+    run_prompt(pool, 4, [0, 63, 700, 64, 500, 10, 1, 127, 0, 300], [1, 4, 2, 0, 4, 9, 3, 1, 2, 4], pad=3)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("G,new", [(8, [1, 1, 1, 1]), (1, [8, 1, 5, 0]), (5, [3, 3, 3, 1]), (7, [1, 1, 1, 1])])
+def test_prompt_few_rows_heads(G, new, causal):
+    # single-token decode through prompt attention; tokens whose heads straddle 8-row tiles
+    pool = Pool("q8_0", 128, 1, 64, 60, seed=21)
+    run_prompt(pool, G, [1500, 0, 333, 1000], new, causal=causal)
+
+
+def test_prompt_few_rows_without_positions():
+    pool = Pool("q4_0", 64, 2, 64, 10, seed=22)
+    run_prompt(pool, 4, [-2, -1, 20], [3, 1, 2])
+
+
 def test_prompt_one_request_many_tokens():
     pool = Pool("q8_0", 128, 1, 64, 12, seed=4)
     run_prompt(pool, 2, [0], [700])
