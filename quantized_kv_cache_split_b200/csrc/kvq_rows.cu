@@ -10,8 +10,8 @@
 //
 //   warps 0-3, 4-7   softmax of row tile 0 / 1 (stream 0 / 1): one thread per row.  Scores
 //                    come from TMEM, weights go back to TMEM as fp16 (the A operand of P V)
-//                    over the scores.  The accumulator is rescaled only when the maximum
-//                    has grown by more than 2^8: until then the weights stay below 2^15.
+//                    over the scores.  The maximum is raised, and the accumulator rescaled,
+//                    only when weights may leave fp16: until then they stay below 2^15.
 //   warps 8-15       dequantize K and V tiles of 128 positions to fp16 in shared memory, four
 //                    warps per half tile.
 //   warp 16          issues the MMAs.
@@ -41,13 +41,13 @@ constexpr int kSoftmaxWarps = 8, kFillWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps + kFillWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // a whole warpgroup for the MMA warp
 // Registers per thread by role, out of 96 x 640 at launch
-constexpr int kSoftmaxRegs = 152, kFillRegs = 72, kMmaRegs = 32;
+constexpr int kSoftmaxRegs = 160, kFillRegs = 64, kMmaRegs = 32;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kFillWarps * kFillRegs + 4 * kMmaRegs) <= 96 * kThreads,
               "register pool");
 constexpr int kOwnWarps = 12, kOwnRegs = 136;  // blocks of own units: three warpgroups of five
 static_assert(32 * (kOwnWarps * kOwnRegs + (kThreads / 32 - kOwnWarps) * kMmaRegs) <= 96 * kThreads, "register pool");
 constexpr float kWeightBits = 7.f;   // weights are 2^(s - m + 7)
-constexpr float kRescaleBits = 8.f;  // growth of the maximum before the accumulator is rescaled
+constexpr float kSafeSum = 32768.f;  // a tile's weights summing to less are all inside fp16
 #ifndef POLY
 #define POLY 0
 #endif
@@ -689,73 +689,91 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
           continue;
         }
         const bool mask = __any_sync(0xffffffffu, lim < kKvTile);
-        float v[kKvTile];
-#pragma unroll
-        for (int c = 0; c < kKvTile; c += 32) tmem_ld32(ts + c, v + c);
-#pragma unroll
-        for (int c = 0; c < kKvTile; c += 32) tmem_wait_ld32(v + c);
-        if (mask) {
-#pragma unroll
-          for (int k = 0; k < kKvTile; ++k) v[k] = k < lim ? v[k] : -INFINITY;
-        }
-        float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int k = 4; k + 8 <= kKvTile; k += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], v[k + 2 * e], v[k + 2 * e + 1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], v[kKvTile - 4 + e]);
-        const float tm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        const bool grow = tm > m + kRescaleBits || (m == -INFINITY && tm > -INFINITY);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2(m - tm) : 1.f;  // m = -inf: 0
-          if (grow) m = tm;
-          l *= f;
-          // the scores of this tile were issued after the last P V of this stream, so the
-          // accumulator is at rest
-          if (i > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 8) {
-              float o[8];
-              tmem_ld8(to + c, o);
-              tmem_wait_ld8(o);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= f;
-              tmem_st8(to + c, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        const float off = m == -INFINITY ? 0.f : kWeightBits - m;
-        const uint64_t off2 = pack_f2(off, off);
-        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of fp32 zeros
-#pragma unroll
-        for (int c = 0; c < kKvTile; c += 64) {
-          uint32_t p[32];
-#pragma unroll
-          for (int k = 0; k < 64; k += 2) {
-            const uint64_t x = fma_f2(pack_f2(v[c + k], v[c + k + 1]), scale2, off2);
-            float e0, e1;
-            if ((k >> 1) % 8 < kPolyPairs) {
-              exp2_poly(x, e0, e1);
-            } else {
-              unpack_f2(x, e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-            }
-            sum[(k >> 1) & 3] = add_f2(sum[(k >> 1) & 3], pack_f2(e0, e1));
-            p[k >> 1] = pack_h2(e0, e1);
-          }
-          tmem_st32(ts + c / 2, p);
-          if (c == 0) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&sh.p_half[s]);
-          }
-        }
+        // No pass over the tile for its maximum: the weights are taken under the maximum that
+        // was last raised, and their sum (which the denominator needs anyway) tells whether one
+        // may have outgrown fp16: below 2^15 none has.  A maximum 2^8 times the old one always
+        // gets there, one that is not above it never does.  Then, and on a row's first
+        // positions, the maximum is raised and the tile done again.
+        bool raise = __any_sync(0xffffffffu, m == -INFINITY && lim > 0);
         float l0, l1;
-        unpack_f2(add_f2(add_f2(sum[0], sum[1]), add_f2(sum[2], sum[3])), l0, l1);
+        uint32_t p[kKvTile / 2];
+        for (;;) {
+          float v[2][32];
+          auto load = [&](int c, float* x) { tmem_ld32(ts + c * 32, x); };
+          auto ready = [&](int c, float* x) {
+            tmem_wait_ld32(x);
+            if (mask) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = c * 32 + k < lim ? x[k] : -INFINITY;
+            }
+          };
+          if (raise) {
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c = 0; c < kKvTile / 32; ++c) {
+              load(c, v[0]);
+              ready(c, v[0]);
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                mx[0] = max3(mx[0], v[0][k], v[0][k + 1]);
+                mx[1] = max3(mx[1], v[0][k + 2], v[0][k + 3]);
+              }
+            }
+            const float tm = fmaxf(mx[0], mx[1]) * scale;
+            const float f = tm > m ? ex2(m - tm) : 1.f;  // m = -inf: 0
+            m = fmaxf(m, tm);
+            l *= f;
+            // the scores of this tile were issued after the last P V of this stream, so the
+            // accumulator is at rest
+            if (i > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 8) {
+                float o[8];
+                tmem_ld8(to + c, o);
+                tmem_wait_ld8(o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] *= f;
+                tmem_st8(to + c, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : kWeightBits - m;
+          const uint64_t off2 = pack_f2(off, off);
+          uint64_t sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
+          load(0, v[0]);
+#pragma unroll
+          for (int c = 0; c < kKvTile / 32; ++c) {
+            float* x = v[c & 1];
+            ready(c, x);
+            if (c + 1 < kKvTile / 32) load(c + 1, v[(c + 1) & 1]);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const uint64_t y = fma_f2(pack_f2(x[k], x[k + 1]), scale2, off2);
+              float e0, e1;
+              if ((k >> 1) % 8 < kPolyPairs) {
+                exp2_poly(y, e0, e1);
+              } else {
+                unpack_f2(y, e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+              }
+              sum[(k >> 1) & 1] = add_f2(sum[(k >> 1) & 1], pack_f2(e0, e1));
+              p[c * 16 + (k >> 1)] = pack_h2(e0, e1);
+            }
+          }
+          unpack_f2(add_f2(sum[0], sum[1]), l0, l1);
+          if (raise || !__any_sync(0xffffffffu, l0 + l1 >= kSafeSum)) break;
+          raise = true;
+        }
+        tmem_st16(ts, p);
+        tmem_st16(ts + 16, p + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh.p_half[s]);
+        tmem_st16(ts + 32, p + 32);
+        tmem_st16(ts + 48, p + 48);
         l += l0 + l1;
         tmem_wait_st();
         tc_fence_before();
