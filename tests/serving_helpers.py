@@ -76,7 +76,8 @@ class Pool:
         relative to the sum by e^(2d) - 1; the weight itself is rounded to fp16 (u), a V value
         by cV u (1, nvfp4 2), and sums of n fp32 terms by 2^-22 each (the tensor core's
         additions truncate).  Each of these scales the average of |v| under the weights.  The
-        smallest fp16 steps add 2^-25 per value and weight."""
+        smallest fp16 steps add 2^-25 per value and, with the largest weight at 2, 2^-26 of it
+        per position."""
         hq, g = q.shape[0], q.shape[0] // self.hkv
         out, bound = np.zeros((hq, self.D)), np.zeros((hq, self.D))
         if len(slots) == 0:
@@ -96,7 +97,7 @@ class Pool:
             o = p @ v
             av = p @ np.abs(v)
             e = np.expm1(2 * d) + (1 + cv) * u + len(slots) * 2.0 ** -22
-            b = av * e + 2.0 ** -24 + len(slots) * 2.0 ** -31 * np.abs(v).max()
+            b = av * e + 2.0 ** -24 + len(slots) * 2.0 ** -26 * np.abs(v).max()
             if self.fmt == "lut4":   # rotated back: each element is a signed mean of all, times sqrt(D)
                 o = OQ.unrotate_f64(o, self.signs)
                 b = np.repeat(b.sum(-1, keepdims=True) / math.sqrt(self.D), self.D, -1)
