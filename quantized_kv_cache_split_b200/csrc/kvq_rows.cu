@@ -307,12 +307,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hkv = a.desc.num_kv_heads, G = a.group;
   grid_dependents_launch();  // the merge may be scheduled (it waits for this grid's results)
-  const int row_blocks = a.row_tiles * hkv * a.splits;
-  if ((int)blockIdx.x >= row_blocks) {
+  // Blocks of own units stand behind the first a.ctas row blocks: those past them have a unit only
+  // when no cut of the groups brings the units down to a.ctas.
+  const int row_blocks = a.row_tiles * hkv * a.splits, own_blocks = (int)gridDim.x - row_blocks;
+  const int own_first = min(row_blocks, a.ctas), own_index = (int)blockIdx.x - own_first;
+  if (own_index >= 0 && own_index < own_blocks) {
     // the requests' own positions: twelve warps, a unit each
     if (warp < kOwnWarps) {
       regs_grow<kOwnRegs>();
-      const int64_t u = (int64_t)(blockIdx.x - row_blocks) * kOwnWarps + warp;
+      const int64_t u = (int64_t)own_index * kOwnWarps + warp;
       if (u < own.units) own_unit<FMT, D>(own, a, u, smem + warp * Own<FMT, D>::kBytes, lane);
     } else {
       regs_shrink<kMmaRegs>();
@@ -320,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
     return;
   }
 
-  if (warp == 0) find_unit(a, blockIdx.x, lane, sh.unit);
+  const int block = own_index < 0 ? (int)blockIdx.x : (int)blockIdx.x - own_blocks;
+  if (warp == 0) find_unit(a, block, lane, sh.unit);
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem, kTmemColumns);
     if (lane == 0) {
