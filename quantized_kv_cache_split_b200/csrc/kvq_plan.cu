@@ -4,9 +4,10 @@
 //
 // One thread-block cluster (one CTA when the step is small): every CTA loads all lengths and
 // runs the same prefix sums, one thread per request, so that no CTA waits for another's
-// result; the tokens and pages are then dealt over the cluster.  Bound by latency: a few
-// dependent reads and three cluster barriers, which stand between the last read of a buffer
-// and its first write (in-place updates) and between the pushes and the pops.
+// result; the pages are then dealt over the cluster.  Bound by latency: a few dependent reads
+// and three cluster barriers, which stand between the last read of a buffer and its first write
+// (in-place updates) and between the pushes and the pops.  The slots of a small step are written
+// by the same CTAs, those of a large one by a second launch over the whole device.
 #include <algorithm>
 
 #include "kvq_device.cuh"
@@ -17,7 +18,8 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;
-constexpr int64_t kSmallStep = 8192;  // slots and pages that one CTA writes by itself
+constexpr int64_t kSmallStep = 8192;   // slots that one CTA writes by itself
+constexpr int64_t kLargeStep = 65536;  // more slots than this: a second launch over the whole device
 static_assert(KVQ_MAX_BATCH <= kPlanThreads, "one thread per request");
 
 struct PlanShared {
@@ -82,8 +84,50 @@ __device__ __forceinline__ uint32_t cluster_or(PlanShared& sh, uint32_t bits, in
   return all;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, int ctas) {
+// Slots and positions of the tokens t0 .. t0 + 3; behind the last token -1 and 0.  tok: first
+// token of each request; old_len(b): its positions before the step; page_of(b, i): its i-th page.
+template <class OldLen, class PageOf>
+__device__ __forceinline__ void write_slots(const PlanArgs& a, int64_t t0, int tokens, const int* tok,
+                                            const OldLen& old_len, const PageOf& page_of) {
+  int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
+  if (t0 < tokens) {
+    int b = owner(tok, a.batch, (int)t0);
+    int n_old = old_len(b);
+    int page_index = -1, page = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = (int)t0 + k;
+      if (t >= tokens) break;
+      if (t >= tok[b + 1]) {
+        do ++b; while (t >= tok[b + 1]);
+        n_old = old_len(b);
+        page_index = -1;
+      }
+      const int p = n_old + t - tok[b];
+      const int pi = (int)((unsigned)p / (unsigned)a.page_size);
+      if (pi != page_index) {
+        page_index = pi;
+        page = page_of(b, pi);
+      }
+      slot[k] = page * a.page_size + (p - pi * a.page_size);
+      pos[k] = p;
+    }
+  }
+  if (t0 + 4 <= a.max_tokens) {
+    *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    if (a.positions) *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+  } else {
+    for (int k = 0; k < 4 && t0 + k < a.max_tokens; ++k) {
+      a.slots[t0 + k] = slot[k];
+      if (a.positions) a.positions[t0 + k] = pos[k];
+    }
+  }
+}
+
+// apart: the slots are left to slots_kernel.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, int ctas, int apart) {
   __shared__ PlanShared sh;
+  grid_dependents_launch();
   const int tid = threadIdx.x;
   const int rank = ctas > 1 ? (int)cluster_rank() : 0;
   const int ps = a.page_size;
@@ -159,42 +203,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
       a.page_table[(int64_t)b * a.max_pages + first + e - sh.need[b]] = a.free_pages[top - 1 - e];
     }
   }
-  // slots and positions, four tokens at a time; behind the last token -1 and 0
   const int tokens = (int)total[0];
-  for (int64_t t0 = (int64_t)at * 4; t0 < a.max_tokens; t0 += (int64_t)step * 4) {
-    int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
-    if (t0 < tokens) {
-      int b = owner(sh.tok, a.batch, (int)t0);
-      int page_index = -1, page = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = (int)t0 + k;
-        if (t >= tokens) break;
-        if (t >= sh.tok[b + 1]) {
-          do ++b; while (t >= sh.tok[b + 1]);
-          page_index = -1;
-        }
-        const int p = sh.old_len[b] + t - sh.tok[b];
-        const int pi = (int)((unsigned)p / (unsigned)ps);
-        if (pi != page_index) {
-          page_index = pi;
-          const int had_b = (int)(((int64_t)sh.old_len[b] + ps - 1) / ps);
-          page = pi < had_b ? a.page_table[(int64_t)b * a.max_pages + pi]
-                            : a.free_pages[top - 1 - (sh.need[b] + pi - had_b)];
-        }
-        slot[k] = page * ps + (p - pi * ps);
-        pos[k] = p;
-      }
-    }
-    if (t0 + 4 <= a.max_tokens) {
-      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      if (a.positions) *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
-      for (int k = 0; k < 4 && t0 + k < a.max_tokens; ++k) {
-        a.slots[t0 + k] = slot[k];
-        if (a.positions) a.positions[t0 + k] = pos[k];
-      }
-    }
+  if (!apart) {
+    for (int64_t t0 = (int64_t)at * 4; t0 < a.max_tokens; t0 += (int64_t)step * 4)
+      write_slots(a, t0, tokens, sh.tok, [&](int b) { return sh.old_len[b]; },
+                  [&](int b, int pi) {
+                    const int had_b = (int)(((int64_t)sh.old_len[b] + ps - 1) / ps);
+                    return pi < had_b ? a.page_table[(int64_t)b * a.max_pages + pi]
+                                      : a.free_pages[top - 1 - (sh.need[b] + pi - had_b)];
+                  });
   }
   if (rank == 0) {
     if (mine) {
@@ -209,9 +226,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
   if (ctas > 1) cluster_sync();  // no CTA leaves while another may still read its bits
 }
 
+// The slots and positions of a large step, over the whole device, from what plan_kernel wrote (a
+// refused step has no tokens).
+constexpr int kSlotThreads = 256;
+__global__ void __launch_bounds__(kSlotThreads) slots_kernel(const PlanArgs a) {
+  __shared__ int tok[KVQ_MAX_BATCH + 1];
+  grid_dependency_wait();
+  for (int b = threadIdx.x; b <= a.batch; b += kSlotThreads) tok[b] = a.token_offsets[b];
+  __syncthreads();
+  const int64_t t0 = ((int64_t)blockIdx.x * kSlotThreads + threadIdx.x) * 4;
+  if (t0 >= a.max_tokens) return;
+  write_slots(a, t0, tok[a.batch], tok, [&](int b) { return a.seq_lens_out[b] - (tok[b + 1] - tok[b]); },
+              [&](int b, int pi) { return a.page_table[(int64_t)b * a.max_pages + pi]; });
+}
+
 }  // namespace
 
 int launch_plan(const PlanArgs& a, cudaStream_t stream) {
+  // Up to kSmallStep slots one CTA (256 tokens: 7 us), then a cluster of eight (37,000 slots: 12 us),
+  // then the cluster for the pages and a second launch, scheduled early, for the slots (494,000
+  // slots: 10 us, against 26 by the cluster alone; the launch itself costs the host 5).
+  const bool apart = (int64_t)a.max_tokens > kLargeStep;
   const int ctas = (int64_t)a.max_tokens > kSmallStep ? kPlanCluster : 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -223,8 +258,19 @@ int launch_plan(const PlanArgs& a, cudaStream_t stream) {
   cfg.blockDim = dim3(kPlanThreads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, plan_kernel, a, ctas) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, plan_kernel, a, ctas, (int)apart) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (!apart) return KVQ_OK;
+  cudaLaunchConfig_t slots = {};
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  slots.gridDim = dim3((unsigned)(((int64_t)a.max_tokens + 4 * kSlotThreads - 1) / (4 * kSlotThreads)), 1, 1);
+  slots.blockDim = dim3(kSlotThreads, 1, 1);
+  slots.stream = stream;
+  slots.attrs = early;
+  slots.numAttrs = 1;
+  return cudaLaunchKernelEx(&slots, slots_kernel, a) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // namespace kvq
