@@ -55,7 +55,8 @@ class QuantizedKVCache:
                                  self.codebook, self.signs)
         self._ws = None
         self._index = _cuda_index(self.device)
-        self._ws_rows = None     # prompt and prefix attention
+        self._ws_rows = {}       # prompt and prefix attention: a workspace per stream
+        self._ws_old = []        # outgrown ones: a captured graph may still use them
         self._rows_bytes = {}    # workspace bytes by request shape
 
     # ---------------------------------------------------------------- writes
@@ -134,10 +135,14 @@ class QuantizedKVCache:
         nbytes = self._rows_bytes.get(key)
         if nbytes is None:
             nbytes = self._rows_bytes[key] = size_fn(self.desc, *args)
-        if self._ws_rows is None or self._ws_rows.numel() < nbytes:
-            self._ws_rows = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-            kb.kvq_workspace_init(self._ws_rows, self._ws_rows.numel(), stream)
-        return out, out_type, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale, stream
+        stream = kb._stream(stream)
+        ws = self._ws_rows.get(stream)
+        if ws is None or ws.numel() < nbytes:
+            if ws is not None:
+                self._ws_old.append(ws)
+            ws = self._ws_rows[stream] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            kb.kvq_workspace_init(ws, ws.numel(), stream)
+        return ws, out, out_type, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale, stream
 
     def prompt_attention(self, q: torch.Tensor, token_offsets: torch.Tensor, seq_lens: torch.Tensor,
                          max_seq_len: int, page_table: Optional[torch.Tensor] = None,
@@ -151,7 +156,10 @@ class QuantizedKVCache:
         and the last ones of its ``seq_lens[b]`` positions (write their K and V first).
         ``causal``: a token sees the positions up to its own.  Rows outside every request are
         padding and keep what ``out`` holds there.  Lengths, offsets and the table are int32
-        tensors on the cache's GPU."""
+        tensors on the cache's GPU.
+
+        The workspace is kept per stream: calls on different streams may overlap, replays of
+        graphs captured on one stream may not."""
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.prompt_attention(q, token_offsets, seq_lens, max_seq_len, page_table, max_pages, causal,
@@ -162,9 +170,8 @@ class QuantizedKVCache:
         if page_table is not None:
             _want("page_table", page_table, torch.int32, self._index, B * max_pages)
         n, Hq = q.shape[0], q.shape[1]
-        out, out_type, sm_scale, stream = self._rows_call("prompt", kb.kvq_prompt_workspace_size, (n, Hq, B, max_seq_len),
+        ws, out, out_type, sm_scale, stream = self._rows_call("prompt", kb.kvq_prompt_workspace_size, (n, Hq, B, max_seq_len),
                                                           q, out, out_dtype, sm_scale, stream)
-        ws = self._ws_rows
         kb.kvq_prompt_attn(self.desc, q, n, Hq, self.k_codes, self.k_scales, self.v_codes, self.v_scales, page_table,
                            max_pages, seq_lens, max_seq_len, token_offsets, B, causal, sm_scale, ws, ws.numel(), out,
                            out_type, stream)
@@ -182,7 +189,8 @@ class QuantizedKVCache:
         one group of all) attends to the ``prefix_lens[g]`` positions of row g of
         ``prefix_table`` and each request to its own ``seq_lens[b]`` positions as well.  The
         prefix is read once per group, not once per request.  Lengths, offsets and tables are
-        int32 tensors on the cache's GPU."""
+        int32 tensors on the cache's GPU.  The workspace is kept per stream (as for
+        prompt_attention)."""
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.prefix_attention(q, prefix_table, prefix_lens, max_prefix_len, seq_lens, max_seq_len,
@@ -202,18 +210,22 @@ class QuantizedKVCache:
         if page_table is not None:
             _want("page_table", page_table, torch.int32, self._index, B * max_pages)
         Hq = q.shape[1]
-        out, out_type, sm_scale, stream = self._rows_call(
+        ws, out, out_type, sm_scale, stream = self._rows_call(
             "prefix", kb.kvq_prefix_workspace_size, (B, Hq, ng, max_prefix_len, max_seq_len), q, out, out_dtype, sm_scale,
             stream)
-        ws = self._ws_rows
         kb.kvq_prefix_attn(self.desc, q, B, Hq, self.k_codes, self.k_scales, self.v_codes, self.v_scales, prefix_table,
                            max_prefix_pages, prefix_lens, max_prefix_len, group_offsets, ng, page_table, max_pages,
                            seq_lens, max_seq_len, sm_scale, ws, ws.numel(), out, out_type, stream)
         return out
 
     def device_flags(self) -> int:
+        """KVQ_FLAG_* bits of the calls so far."""
         flags = 0 if self._ws is None else kb.kvq_read_device_flags(self._ws)
-        return flags if self._ws_rows is None else flags | kb.kvq_read_device_flags(self._ws_rows)
+        if self._ws_rows:
+            torch.cuda.synchronize(self._index)  # their streams
+            for ws in (*self._ws_rows.values(), *self._ws_old):
+                flags |= kb.kvq_read_device_flags(ws)
+        return flags
 
 
 def _want(name: str, t: torch.Tensor, dtype: torch.dtype, index: int, numel: Optional[int] = None) -> None:

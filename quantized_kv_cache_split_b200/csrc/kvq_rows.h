@@ -46,7 +46,8 @@ struct RowsArgs {
 };
 
 // Decode of single tokens over their own positions in the same launch (kvq_own.cuh): token b's
-// positions 0 .. seq_lens[b] - 1, cut at multiples of split.  units = 0: none.
+// positions 0 .. seq_lens[b] - 1, cut at multiples of split.  units = 0: none has any; seq_lens
+// null: not a prefix decode.
 struct OwnArgs {
   int64_t units;           // n_tokens * num_kv_heads * max_splits, one warp each
   const int32_t* table;    // [n_tokens][max_pages], or null: pages b*max_pages ..
@@ -68,8 +69,8 @@ size_t rows_partial_bytes(int n_tokens, int num_q_heads, int head_dim, int split
 int plan_own(int num_kv_heads, int batch, int max_seq_len, int* ctas);
 
 int launch_rows(const RowsArgs& a, const OwnArgs& own, cudaStream_t stream);
-// Merge of the partials of a rows launch (own.units > 0: those of the own positions as well)
-// into the normalized output; lut4 is rotated back.
+// Merge of the partials of a rows launch (own.seq_lens: those of the own positions as well) into
+// the normalized output; lut4 is rotated back.
 int launch_rows_merge(const RowsArgs& a, const OwnArgs& own, void* out, int out_f16, cudaStream_t stream);
 
 // The visible positions of token i of a group of n tokens and `len` positions.

@@ -95,13 +95,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergeArgs
     if (len < 0 || len > r.max_len || len > (int64_t)r.max_pages * r.desc.page_size) len = 0;
     lim = min(len, row_limit(len, n, token - first, r.causal));
   }
-  if (a.own.units > 0) {
+  if (a.own.seq_lens) {  // prefix decode
     int len = a.own.seq_lens[token];
     if (len < 0 || len > a.own.max_seq_len || len > (int64_t)a.own.max_pages * r.desc.page_size) len = 0;
     no = (len + a.own.split - 1) / a.own.split;
   }
   grid_dependency_wait();  // the partials and the chunk
-  if (!found && a.own.units == 0) return;  // a token behind the last request: left as it was
+  if (!found && !a.own.seq_lens) return;  // a token behind the last request: left as it was
   const int chunk = r.splits > 1 ? *reinterpret_cast<volatile int32_t*>(r.chunk_out) : r.min_chunk;
   if (lim > 0) ns = (int)(((int64_t)lim + chunk - 1) / chunk);
   const float* pm = r.part_m + row * r.splits;

@@ -331,6 +331,104 @@ def test_prefix_without_own_positions():
     run_prefix(pool, 2, [800], [5], [0] * 5)
 
 
+def test_prefix_no_own_positions_anywhere():
+    # max_seq_len 0: requests outside every group have no position at all and get zeros
+    pool = Pool("lut4", 64, 1, 64, 12, seed=23)
+    q = dev(pool.queries(4, 2), np.float16)
+    out = torch.full((4, 2, 64), 3.0, device="cuda")
+    pool.cache.prefix_attention(q, dev([[5, 6, 7]]), dev([150]), 192, dev([0, 0, 0, 0]), 0, None, 1,
+                                group_offsets=dev([1, 3]), out=out)
+    got = out.cpu().numpy()
+    assert not got[0].any() and not got[3].any()
+    for b in (1, 2):
+        want, bound = pool.attend(q.cpu().numpy()[b], pool.slots_of([5, 6, 7], 150), 1 / 8)
+        check_close(got[b], want, bound, False)
+    # and no prefix either
+    pool.cache.prefix_attention(q, dev([[5, 6, 7]]), dev([0]), 0, dev([0, 0, 0, 0]), 0, None, 1, out=out)
+    assert not out.any()
+
+
+def test_prefix_40_groups():
+    # more groups than lanes of a warp
+    pool = Pool("q4_0", 64, 1, 64, 150, seed=24)
+    prefix = list(pool.rng.integers(0, 130, 40))
+    run_prefix(pool, 2, prefix, [1, 2] * 20, list(pool.rng.integers(0, 60, 60)))
+
+
+def test_prompt_many_requests():
+    pool = Pool("q8_0", 64, 1, 64, 200, seed=25)
+    old, new = pool.rng.integers(0, 100, 70), pool.rng.integers(0, 40, 70)
+    run_prompt(pool, 4, old, new)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_prompt_growing_scores(fmt):
+    # keys whose scores grow by far more than fp16's range from block to block, and fall again:
+    # the maximum is raised many times
+    pool = Pool(fmt, 128, 1, 64, 16, seed=26)
+    n = 900
+    grow = np.concatenate((np.linspace(0, 60, n // 2), np.linspace(60, -60, n - n // 2)))[:, None, None]
+    k = (grow * pool.u / math.sqrt(128) + 0.1 * pool.rng.standard_normal((n, 1, 128))).astype(np.float16)
+    v = pool.rng.standard_normal((n, 1, 128)).astype(np.float16)
+    pool.cache.write(dev(k, np.float16), dev(v, np.float16), dev(np.arange(n)))
+    pool.k, pool.v = pool.values("k"), pool.values("v")
+    q = (pool.u + 0.1 * pool.rng.standard_normal((200, 2, 128))).astype(np.float16)
+    out = pool.cache.prompt_attention(dev(q, np.float16), dev([0, 200]), dev([n]), n, dev([np.arange(16)]), 16).cpu().numpy()
+    for i in (0, 1, 77, 199):
+        want, bound = pool.attend(q[i], np.arange(n - 200 + i + 1), 1 / math.sqrt(128))
+        check_close(out[i], want, bound, False)
+
+
+def test_two_streams_at_once():
+    # calls on two streams that overlap: a workspace each
+    pool = Pool("q4_0", 128, 2, 64, 60, seed=27)
+    qs = [dev(pool.queries(40, 8), np.float16) for _ in range(2)]
+    tab = [dev([np.arange(30)]), dev([np.arange(30, 60)])]
+    alone = [pool.cache.prefix_attention(qs[i], tab[i], dev([1900]), 1920, dev([0] * 40), 0).clone() for i in range(2)]
+    own = dev([0] * 40)
+    lens = dev([1900])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(pool.cache.prefix_attention(qs[i], tab[i], lens, 1920, own, 0))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, alone[i]) for o in outs[i])
+
+
+def test_results_repeat_bit_for_bit():
+    pool = Pool("q8_0", 128, 2, 64, 60, seed=28)
+    q = dev(pool.queries(50, 8), np.float16)
+    args = (q, dev([np.arange(40)]), dev([2500]), 2560, dev(pool.rng.integers(0, 20, 50)), 64,
+            dev(np.tile(np.arange(40, 60), 3)[:50].reshape(50, 1)), 1)
+    first = pool.cache.prefix_attention(*args)
+    assert all(torch.equal(first, pool.cache.prefix_attention(*args)) for _ in range(5))
+
+
+def test_methods_refuse_what_the_kernels_cannot_read():
+    pool = Pool("q4_0", 128, 2, 64, 8, seed=29)
+    c = pool.cache
+    q = dev(pool.queries(4, 8), np.float16)
+    off, lens, tab = dev([0, 4]), dev([100]), dev([[0, 1]])
+    ok = lambda **kw: c.prompt_attention(**{**dict(q=q, token_offsets=off, seq_lens=lens, max_seq_len=128,  # noqa: E731
+                                                  page_table=tab, max_pages=2), **kw})
+    ok()
+    wide = torch.zeros(4, 16, 128, dtype=torch.float16, device="cuda")
+    for bad in (dict(q=wide[:, ::2]), dict(q=q.float()), dict(q=q[..., :64].contiguous()), dict(q=q.cpu()),
+                dict(token_offsets=off.long()), dict(token_offsets=dev([0])), dict(seq_lens=lens.cpu()),
+                dict(page_table=dev([[0, 1, 2, 3]])[:, ::2]), dict(max_pages=3), dict(out=torch.empty_like(q[:2])),
+                dict(out=q.bfloat16()), dict(out_dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            ok(**bad)
+    with pytest.raises(ValueError):
+        c.prefix_attention(q, None, lens, 128, dev([0] * 4), 0)
+    with pytest.raises(ValueError):
+        c.prefix_attention(q, tab, lens, 128, dev([0] * 3), 0)
+
+
 def test_prefix_and_decode_agree():
     # a request whose whole sequence is its own, or half of it the prefix: kvq_decode_attn's answer
     pool = Pool("q8_0", 128, 2, 64, 20, seed=16)
