@@ -122,7 +122,7 @@ class QuantizedKVCache:
             raise ValueError(f"q must be [tokens, heads, {D}], not {tuple(q.shape)}")
         _want("q", q, torch.float16, self._index)
         if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype, device=self.device)
+            out = torch.empty_like(q) if out_dtype is torch.float16 else torch.empty_like(q, dtype=out_dtype)
         elif out.shape != q.shape:
             raise ValueError(f"out must have q's shape {tuple(q.shape)}, not {tuple(out.shape)}")
         out_type = _OUT_TYPES.get(out.dtype)

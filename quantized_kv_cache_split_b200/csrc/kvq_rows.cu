@@ -359,6 +359,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
   const int tiles = end > begin ? (end - begin + kKvTile - 1) / kKvTile : 0;
   const bool shared_tiles = rows > 128;  // both streams take every tile; else every other one
   const bool live = n > 0 && (tiles > 0 || a.out != nullptr);
+  // row r of the unit: token tok_base + t, head h of the KV head's G, t = (r + h_base) / G by a 16-bit
+  // reciprocal (exact below 8192)
+  const int tok_base = row0 / G, h_base = row0 - tok_base * G;
+  const uint32_t g_inv = 65536u / (uint32_t)G + 1u;
+  auto token_of = [&](int r) { return tok_base + (int)(((uint32_t)(r + h_base) * g_inv) >> 16); };
+  auto row_index = [&](int r) {  // in q, the output and the partials
+    const int t = token_of(r);
+    return (int64_t)(tok0 + t) * a.num_q_heads + kvh * G + (row0 + r - t * G);
+  };
   const int stages = shared_tiles ? S::kStages : S::kStages + S::kExtra;
   auto stage_at = [&](int st) {
     return smem + (st < S::kStages ? S::kRaw + st * S::kRawBytes : S::kQ + S::kTileBytes + (st - S::kStages) * S::kRawBytes);
@@ -592,16 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       // query rows, fp16, K-major, 128-byte swizzle; rows past the unit's are zero.  The loads
       // of several rows are in flight together.  A unit of one row tile has one for both streams.
       {
-        const __half* q = static_cast<const __half*>(a.q) + (int64_t)kvh * G * D;
+        const __half* q = static_cast<const __half*>(a.q);
         const bool zero = a.sm_scale == 0.f;
         const uint32_t flip = a.sm_scale < 0.f ? 0x80008000u : 0u;  // the scale's sign goes into the query
         const int n_rows = shared_tiles ? kRowTile : 128;
-        auto src = [&](int r) {
-          const int t = (row0 + r) / G;
-          return q + ((int64_t)(tok0 + t) * a.num_q_heads + (row0 + r - t * G)) * D;
-        };
+        auto src = [&](int r) { return q + row_index(r) * D; };
         if constexpr (!C::kLut) {
-          constexpr int kC = D / 8, kStep = 32 * kSoftmaxWarps / kC, kBatch = 8;
+          constexpr int kC = D / 8, kStep = 32 * kSoftmaxWarps / kC, kBatch = 16;
           const int c = tid % kC;
           for (int r0 = tid / kC; r0 < n_rows; r0 += kBatch * kStep) {
             uint4 v[kBatch];
@@ -676,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       const int rr = shared_tiles ? s * 128 + r : r;
       const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
       const float scale = (a.sm_scale == 0.f ? 1.f : fabsf(a.sm_scale)) * kLog2e * kUnhalve<FMT>;
-      const int limit = rr < rows ? min(row_limit(len, n, (row0 + rr) / G, a.causal), end) : end;
+      const int limit = rr < rows ? min(row_limit(len, n, token_of(rr), a.causal), end) : end;
       const int steps = shared_tiles ? tiles : (tiles - s + 1) / 2;
       const uint32_t ts = at + s * 128, to = at + 256 + s * D;  // scores, accumulator
       const uint64_t scale2 = pack_f2(scale, scale);
@@ -827,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
       // every lane takes part in the TMEM loads; rows past the unit's are not written
       if (shared_tiles || s == 0) {
         const bool write = ok && rr < rows, half = a.out && a.out_f16;
-        const int64_t row = write ? (int64_t)(tok0 + (row0 + rr) / G) * a.num_q_heads + kvh * G + (row0 + rr) % G : 0;
+        const int64_t row = write ? row_index(rr) : 0;
         const int64_t part = row * a.splits + split;
         // every tile has been read: the query and K / V space holds the rows (16 bytes of
         // padding between them), each copied out by the thread that owns it
@@ -871,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
     }
   } else if (live && warp < kSoftmaxWarps && tid < rows) {
     // no position at all: the rows are zero
-    const int64_t row = (int64_t)(tok0 + (row0 + tid) / G) * a.num_q_heads + kvh * G + (row0 + tid) % G;
+    const int64_t row = row_index(tid);
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * (a.out_f16 ? 2 : 4));
     for (int k = 0; k < D * (a.out_f16 ? 2 : 4) / 16; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
   }
