@@ -383,13 +383,16 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  *                0: every position.  A token that sees none gets zeros.
  *   sm_scale     score scale, finite, of any sign
  *   workspace    device, kvq_prompt_workspace_size(...) bytes, 16-byte aligned, initialized
- *                once with kvq_workspace_init; also used by kvq_prefix_attn calls if it is large
- *                enough, but not by kvq_decode_attn
+ *                once with kvq_workspace_init; kvq_prefix_attn calls may use it too if it is
+ *                large enough, kvq_decode_attn calls may not.  Calls that share a workspace must
+ *                not overlap on the GPU.
  *   out          device [n_tokens][num_q_heads][head_dim] of out_type, 16-byte aligned
  *   out_type     KVQ_OUT_F32 or KVQ_OUT_F16 (one rounding of the fp32 result)
- * K and V values are rounded to fp16 once dequantized, the weights to fp16 for the product
- * with V; scores, softmax statistics and sums are fp32.
- * Same limits as kvq_decode_attn (KVQ_MAX_GROUP, KVQ_MAX_BATCH); max_seq_len <= 2^30.
+ * Roundings: K and V values to fp16 once dequantized (nvfp4: first the block scale times the
+ * vector scale; lut4: the rotated query as well), the weights to fp16 for the product with V;
+ * scores, softmax statistics and sums are fp32.  Results do not depend on timing: the same
+ * call gives the same bits.
+ * Same limits as kvq_decode_attn (KVQ_MAX_GROUP, KVQ_MAX_BATCH); lengths up to 2^29.
  * Sequences whose length, offsets or pages are out of range set KVQ_FLAG_BAD_SEQLEN /
  * KVQ_FLAG_BAD_PAGE and nothing outside the buffers is touched.
  */
@@ -417,6 +420,8 @@ int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
  *   page_table, max_pages, seq_lens, max_seq_len   the requests' own positions, as for
  *                kvq_decode_attn (page_table NULL: pages b*max_pages ..); a length may be 0
  *   other arguments as for kvq_prompt_attn; the workspace is kvq_prefix_workspace_size(...)
+ * The requests' own positions are meant to be the shorter part (a warp per request, KV head and
+ * split); K there is not rounded to fp16 for q8_0, q4_0 and lut4.
  * A request without any position gets zeros.
  */
 int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_t num_q_heads,

@@ -276,29 +276,6 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^x of two values on the FMA pipe (the special-function unit gives 16 a clock and SM): x is
-// split into the nearest integer n (by adding 1.5 2^23, whose last place is 1) and f in
-// [-1/2, 1/2]; 2^f is the degree-4 polynomial of least relative error there (2.6e-6, found
-// by exchange over a grid), and n is added to its exponent.  Below 2^-100: 2^-100.
-__device__ __forceinline__ void exp2_poly(uint64_t x2, float& e0, float& e1) {
-  float x0, x1;
-  unpack_f2(x2, x0, x1);
-  x2 = pack_f2(fmaxf(x0, -100.f), fmaxf(x1, -100.f));
-  const float kBig = 12582912.f;
-  const uint64_t t = add_f2(x2, pack_f2(kBig, kBig));
-  const uint64_t n = add_f2(t, pack_f2(-kBig, -kBig));
-  const uint64_t f = fma_f2(n, pack_f2(-1.f, -1.f), x2);
-  uint64_t p = fma_f2(f, pack_f2(0.009570102207362652f, 0.009570102207362652f),
-                      pack_f2(0.05591785907745361f, 0.05591785907745361f));
-  p = fma_f2(p, f, pack_f2(0.240247443318367f, 0.240247443318367f));
-  p = fma_f2(p, f, pack_f2(0.6931217908859253f, 0.6931217908859253f));
-  p = fma_f2(p, f, pack_f2(0.9999992847442627f, 0.9999992847442627f));
-  float t0, t1, p0, p1;
-  unpack_f2(t, t0, t1);
-  unpack_f2(p, p0, p1);
-  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

@@ -22,9 +22,22 @@
 // tile is dequantized once for 256 rows.  A unit of at most 128 rows gives both streams
 // the same rows and every other tile each; the streams' results are merged at the end.
 //
-// Roundings: K and V values to fp16 (2^-11 relative, as code * scale; nvfp4 first its block
-// scale times vector scale), the lut4 query after its rotation to fp16, the weights to fp16.  Scores, maxima, sums
-// and accumulators are fp32.
+// Own positions of prefix decode are units of one warp (kvq_own.cuh) in blocks of the same grid.
+//
+// Roundings: K and V values to fp16 (2^-11 relative, as code * scale; nvfp4 first its block scale
+// times vector scale), the lut4 query after its rotation to fp16, the weights to fp16: the
+// operand types of the tensor core.  Scores, maxima, sums and accumulators are fp32.
+//
+// What bounds it.  256 rows x 128 positions at head_dim 128: the MMAs alone 2048 clocks, the
+// exponentials alone 2048 (16 a clock and SM), shared memory about 2600 (the fp16 tiles written
+// and read by the MMAs, the query read again for every tile, the staged codes); measured 3900.
+// Both streams alternate: one's weights are computed while the other's MMAs run.  Measured on a
+// 64K q8_0 prefix for 256 requests (32/4 heads, 275 GFLOP): 290 us alone, 950 TFLOP/s, 330 in a
+// sustained loop under the power cap; tensor pipe 56 % busy on the SMs at work, exponentials 57 %,
+// issue slots 60 %.  Tried and slower there: 64-position tiles with two score buffers per stream
+// (345 us), two threads per row (370, register spills), a quarter of the exponentials on the FMA
+// pipe (358), a pass for the tile's maximum (321).
+// 128 rows or fewer: 2550 clocks for 128 positions, bound by dequantizing through shared memory.
 #include <math.h>
 
 #include <algorithm>
@@ -51,10 +64,6 @@ static_assert(32 * (kOwnWarps * kOwnRegs + (kThreads / 32 - kOwnWarps) * kMmaReg
 // took 247 us instead of 236)
 constexpr float kWeightBits = 1.f;
 constexpr float kSafeSum = 32768.f;  // a tile's weights summing to less are all inside fp16
-#ifndef POLY
-#define POLY 0
-#endif
-constexpr int kPolyPairs = POLY;        // of 8 pairs of weights, those computed on the FMA pipe
 constexpr uint32_t kTmemColumns = 512;
 // q8_0 and nvfp4 values enter the products halved (their rounded code * scale can pass the
 // largest fp16 value by a step); the factor goes into the score scale and the output.
@@ -766,13 +775,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
             for (int k = 0; k < 32; k += 2) {
               const uint64_t y = fma_f2(pack_f2(x[k], x[k + 1]), scale2, off2);
               float e0, e1;
-              if ((k >> 1) % 8 < kPolyPairs) {
-                exp2_poly(y, e0, e1);
-              } else {
-                unpack_f2(y, e0, e1);
-                e0 = ex2(e0);
-                e1 = ex2(e1);
-              }
+              unpack_f2(y, e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
               sum[(k >> 1) & 1] = add_f2(sum[(k >> 1) & 1], pack_f2(e0, e1));
               p[c * 16 + (k >> 1)] = pack_h2(e0, e1);
             }

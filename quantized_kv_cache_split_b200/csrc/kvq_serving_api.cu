@@ -12,7 +12,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kMaxLen = 1 << 30;
+constexpr int kMaxLen = 1 << 29;
 constexpr int kChunkWord = 40;  // 32-bit word of the workspace header that holds the rows launch's chunk
 
 // What kvq_prompt_attn and kvq_prefix_attn ask of a request besides its pointers.
