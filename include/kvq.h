@@ -379,6 +379,8 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  *   k_codes .. page_table, max_pages   as for kvq_decode_attn
  *   seq_lens     device int32 [batch]: positions of each sequence, the new tokens included, in
  *                [0, min(max_seq_len, max_pages*page_size)]
+ *                (For a batch of single tokens kvq_decode_attn is the faster call: here every
+ *                request's rows take a tensor-core tile of 128.)
  *   causal       1: token i of request b sees the positions 0 .. seq_lens[b] - n_b + i;
  *                0: every position.  A token that sees none gets zeros.
  *   sm_scale     score scale, finite, of any sign

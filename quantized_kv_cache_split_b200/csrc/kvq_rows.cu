@@ -204,103 +204,107 @@ __device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8
 }
 
 // ------------------------------------------------------------------ unit lookup
+// A group's tokens and positions, checked; the tokens are 0 when they are out of range.
+struct Group {
+  int first, tokens, len;
+};
+__device__ __forceinline__ Group read_group(const RowsArgs& a, int g) {
+  const int first = a.offsets ? a.offsets[g] : 0, end = a.offsets ? a.offsets[g + 1] : a.n_tokens;
+  int len = a.lens[g];
+  const bool bad_len = len < 0 || len > a.max_len || len > (int64_t)a.max_pages * a.desc.page_size;
+  const bool bad = first < 0 || end < first || end > a.n_tokens;
+  if (bad || bad_len) set_flag(a.flags, KVQ_FLAG_BAD_SEQLEN);
+  return Group{first, bad ? 0 : end - first, bad_len ? 0 : len};
+}
+
 // Block `t`'s unit: group, first row, rows, positions, first token, tokens (0: no such unit), KV
-// head, split, positions per split.  One warp; the lanes take consecutive ranges of groups.  The
-// chunk balances groups of unequal lengths (up to 32 groups): about the shortest multiple of kKvTile
-// for which the units (row tile, KV head, split) number at most a.ctas.
+// head, split, positions per split.  One warp.
+//
+// Up to 32 groups: one per lane, units counted exactly.  The chunk balances groups of unequal
+// lengths: about the shortest multiple of kKvTile for which the units (row tile, KV head, split)
+// number at most a.ctas.
+// More groups: the row tiles of group g (rows s .. e - 1 of all groups' rows) take the slots from
+// floor(s / kRowTile) + g, which leaves room for ceil((e - s) / kRowTile) of them, so that a block
+// finds its group by a search instead of a sum over all groups.  The chunk is a.min_chunk.
 __device__ __forceinline__ void find_unit(const RowsArgs& a, int t, int lane, int* unit) {
-  const int per = (a.num_groups + 31) / 32, hkv = a.desc.num_kv_heads;
-  const int g0 = min(lane * per, a.num_groups), g1 = min(g0 + per, a.num_groups);
-  auto group = [&](int g, int& first, int& len) {  // tokens
-    first = a.offsets ? a.offsets[g] : 0;
-    const int end = a.offsets ? a.offsets[g + 1] : a.n_tokens;
-    len = a.lens[g];
-    if (len < 0 || len > a.max_len || len > (int64_t)a.max_pages * a.desc.page_size) {
-      set_flag(a.flags, KVQ_FLAG_BAD_SEQLEN);
-      len = 0;
-    }
-    if (first < 0 || end < first || end > a.n_tokens) {
-      set_flag(a.flags, KVQ_FLAG_BAD_SEQLEN);
-      return 0;
-    }
-    return end - first;
-  };
+  const int hkv = a.desc.num_kv_heads;
   auto tiles_of = [&](int n) { return (n * a.group + kRowTile - 1) / kRowTile; };
   // splits of a group; with direct output a unit without positions still writes its zeros
   auto splits_of = [&](int len, int chunk) { return max((len + chunk - 1) / chunk, a.out ? 1 : 0); };
-  int first0 = 0, len0 = 0, n0 = 0;  // of group g0 (the only one of this lane when per is 1)
-  if (g0 < g1) n0 = group(g0, first0, len0);
-  auto units = [&](int chunk) {  // of this lane's groups
-    int u = 0;
-    for (int g = g0; g < g1; ++g) {
-      int first = first0, len = len0;
-      const int n = g == g0 ? n0 : group(g, first, len);
-      u += tiles_of(n) * splits_of(len, chunk) * hkv;
-    }
-    return u;
+  auto put = [&](int g, const Group& x, int row_tile, int head, int split, int chunk) {
+    // the last rows of a causal group see the most positions: they start first
+    const int tile = a.causal ? tiles_of(x.tokens) - 1 - row_tile : row_tile;
+    unit[0] = g;
+    unit[1] = tile * kRowTile;
+    unit[2] = min(x.tokens * a.group - tile * kRowTile, kRowTile);
+    unit[3] = x.len;
+    unit[4] = x.first;
+    unit[5] = x.tokens;
+    unit[6] = head;
+    unit[7] = split;
+    unit[8] = chunk;
   };
+  if (lane == 0) unit[5] = 0;
+  __syncwarp();
   int chunk = a.min_chunk;
+  if (a.num_groups > 32) {
+    if (a.splits > 1 && t == 0 && lane == 0) *a.chunk_out = chunk;
+    const int split = t % a.splits, head = t / a.splits % hkv, slot = t / a.splits / hkv;
+    auto first_slot = [&](int g) { return (int)((int64_t)a.offsets[g] * a.group / kRowTile) + g; };
+    int lo = 0, hi = a.num_groups - 1;  // the last group whose first slot is not behind this one
+    while (lo < hi) {
+      const int step = (hi - lo + 31) >> 5;
+      const int k = __popc(__ballot_sync(0xffffffffu, first_slot(min(lo + (lane + 1) * step, hi)) <= slot));
+      const int next = min(lo + k * step, hi);
+      if (k < 32) hi = max(next, min(lo + (k + 1) * step, hi) - 1);
+      lo = next;
+    }
+    if (lane == 0) {
+      const Group x = read_group(a, lo);
+      const int row_tile = slot - first_slot(lo);
+      if (row_tile >= 0 && row_tile < tiles_of(x.tokens) && split < splits_of(x.len, chunk))
+        put(lo, x, row_tile, head, split, chunk);
+    }
+    __syncwarp();
+    return;
+  }
+  Group x{0, 0, 0};
+  if (lane < a.num_groups) x = read_group(a, lane);
+  const int tiles = tiles_of(x.tokens);
   if (a.splits > 1) {
     // In tiles of kKvTile.  32 candidates at a time, one per lane, between the even share of all
     // the work and the longest group; then again around the best.  (The candidates' units by
     // approximate reciprocals: a unit more or less than a.ctas only costs balance.)
-    const int t0 = tiles_of(n0) * hkv, l0 = (len0 + kKvTile - 1) / kKvTile;
-    int lo, hi = max(a.min_chunk / kKvTile, 1);
-    lo = hi;
-    if (per == 1) {
-      const float share = (float)__reduce_add_sync(0xffffffffu, (unsigned)(t0 * l0)) / (float)a.ctas;
-      lo = max(lo, (int)ceilf(share));
-      hi = max(lo, (int)__reduce_max_sync(0xffffffffu, (unsigned)l0));
-      for (int pass = 0; pass < 2 && lo < hi; ++pass) {
-        const int step = (hi - lo + 31) >> 5;
-        const int c = min(lo + lane * step, hi);
-        const float r = __frcp_rn((float)c);
-        int u = 0;
-        for (int g = 0; g < a.num_groups; ++g)
-          u += __shfl_sync(0xffffffffu, t0, g) * (int)ceilf((float)__shfl_sync(0xffffffffu, l0, g) * r - 1e-3f);
-        const uint32_t fits = __ballot_sync(0xffffffffu, u <= a.ctas);
-        const int k = fits ? __ffs(fits) - 1 : 32;
-        hi = min(lo + k * step, hi);
-        lo = k > 0 ? min(lo + (k - 1) * step + 1, hi) : lo;
-      }
+    const int t0 = tiles * hkv, l0 = (x.len + kKvTile - 1) / kKvTile;
+    const float share = (float)__reduce_add_sync(0xffffffffu, (unsigned)(t0 * l0)) / (float)a.ctas;
+    int lo = max(max(a.min_chunk / kKvTile, 1), (int)ceilf(share));
+    int hi = max(lo, (int)__reduce_max_sync(0xffffffffu, (unsigned)l0));
+    for (int pass = 0; pass < 2 && lo < hi; ++pass) {
+      const int step = (hi - lo + 31) >> 5;
+      const int c = min(lo + lane * step, hi);
+      const float r = __frcp_rn((float)c);
+      int u = 0;
+      for (int g = 0; g < a.num_groups; ++g)
+        u += __shfl_sync(0xffffffffu, t0, g) * (int)ceilf((float)__shfl_sync(0xffffffffu, l0, g) * r - 1e-3f);
+      const uint32_t fits = __ballot_sync(0xffffffffu, u <= a.ctas);
+      const int k = fits ? __ffs(fits) - 1 : 32;
+      hi = min(lo + k * step, hi);
+      lo = k > 0 ? min(lo + (k - 1) * step + 1, hi) : lo;
     }
     chunk = hi * kKvTile;
     if (t == 0 && lane == 0) *a.chunk_out = chunk;
   }
-  const int mine = units(chunk);
+  const int splits = splits_of(x.len, chunk), mine = tiles * splits * hkv;
   int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
+    const int y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
   }
   before -= mine;
-  if (lane == 0) unit[5] = 0;
-  __syncwarp();
-  if (t >= before && t < before + mine) {
-    int k = t - before;
-    for (int g = g0; g < g1; ++g) {
-      int first = first0, len = len0;
-      const int n = g == g0 ? n0 : group(g, first, len);
-      const int tiles = tiles_of(n), splits = splits_of(len, chunk);
-      if (k < tiles * splits * hkv) {
-        // split fastest, then KV head; the last rows of a causal group see the most positions:
-        // they start first
-        const int row_tile = k / splits / hkv;
-        const int tile = a.causal ? tiles - 1 - row_tile : row_tile;
-        unit[0] = g;
-        unit[1] = tile * kRowTile;
-        unit[2] = min(n * a.group - tile * kRowTile, kRowTile);
-        unit[3] = len;
-        unit[4] = first;
-        unit[5] = n;
-        unit[6] = k / splits % hkv;
-        unit[7] = k % splits;
-        unit[8] = chunk;
-        break;
-      }
-      k -= tiles * splits * hkv;
-    }
+  if (t >= before && t < before + mine) {  // split fastest, then KV head
+    const int k = t - before;
+    put(lane, x, k / splits / hkv, k / splits % hkv, k % splits, chunk);
   }
   __syncwarp();
 }
@@ -334,6 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
 
   const int block = own_index < 0 ? (int)blockIdx.x : (int)blockIdx.x - own_blocks;
   if (warp == 0) find_unit(a, block, lane, sh.unit);
+  // (many groups: the search looks at a few of them; one block checks them all)
+  if (warp == kCopyWarp + 1 && block == 0 && a.num_groups > 32)
+    for (int g = lane; g < a.num_groups; g += 32) (void)read_group(a, g);
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem, kTmemColumns);
     if (lane == 0) {
@@ -930,7 +937,8 @@ int launch_t(const RowsArgs& a, const OwnArgs& own, cudaStream_t stream) {
 RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, int max_len, int ctas) {
   RowsPlan p;
   const int64_t rows = (int64_t)n_tokens * group;
-  p.row_tiles = (int)((rows + (int64_t)num_groups * (kRowTile - 1)) / kRowTile);
+  p.row_tiles = num_groups > 32 ? (int)(rows / kRowTile + num_groups)  // find_unit's slots
+                                : (int)((rows + (int64_t)num_groups * (kRowTile - 1)) / kRowTile);
   const int64_t units = std::max<int64_t>(1, (int64_t)p.row_tiles * num_kv_heads);
   int64_t want = std::max<int64_t>(1, ctas / units);
   if (num_groups > 1 && num_groups <= 32 && want > 1) want = std::min<int64_t>(4 * want, std::max(1, ctas / num_kv_heads));

@@ -361,6 +361,44 @@ def test_prompt_many_requests():
     run_prompt(pool, 4, old, new)
 
 
+@pytest.mark.parametrize("batch", [33, 300, 1024])
+def test_prompt_batches_of_many_groups(batch):
+    # the search for a block's group: many requests, some without tokens, some of several row tiles
+    pool = Pool("q4_0", 64, 1, 64, 1100, seed=30)
+    new = pool.rng.integers(0, 2, batch)
+    new[batch // 2], new[batch // 3], new[-1] = 150, 65, 70
+    old = np.where(pool.rng.random(batch) < 0.1, 40, 0)
+    run_prompt(pool, 4, old, new, pad=2)
+
+
+def test_prompt_many_groups_flag_bad_ones():
+    import quantized_kv_cache_split_b200 as K
+    pool = Pool("q8_0", 64, 1, 64, 8, seed=31)
+    q = dev(pool.queries(40, 2), np.float16)
+    off, lens = np.arange(41), np.full(40, 5)
+    for what in ("len", "offset"):
+        o, n = off.copy(), lens.copy()
+        if what == "len":
+            n[37] = 200
+        else:
+            o[21] = 0
+        cache = K.QuantizedKVCache("q8_0", 64, 1, 64, 8)
+        cache.prompt_attention(q, dev(o), dev(n), 128, dev(np.zeros((40, 2))), 2)
+        assert cache.device_flags() == K.KVQ_FLAG_BAD_SEQLEN, what
+
+
+def test_prompt_padding_before_the_first_request():
+    pool = Pool("q8_0", 64, 1, 64, 8, seed=32)
+    q = pool.queries(9, 2)
+    out = torch.full((9, 2, 64), 5.0, device="cuda")
+    pool.cache.prompt_attention(dev(q, np.float16), dev([3, 7]), dev([100]), 128, dev([[4, 2]]), 2, out=out)
+    got = out.cpu().numpy()
+    assert (got[:3] == 5.0).all() and (got[7:] == 5.0).all()
+    for i in range(4):
+        want, bound = pool.attend(q[3 + i], pool.slots_of([4, 2], 100)[:97 + i], 1 / 8)
+        check_close(got[3 + i], want, bound, False)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_prompt_growing_scores(fmt):
     # keys whose scores grow by far more than fp16's range from block to block, and fall again:
