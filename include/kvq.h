@@ -370,6 +370,8 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  *   (No passage: the pages' kernel has one query token.  Dense softmax attention; the skip
  *   threshold is for kvq_decode_attn: over hundreds of query rows some row keeps nearly
  *   every position.)
+ * Any number of tokens per request; for a batch of single tokens kvq_decode_attn is the
+ * faster call (here the rows of every request take a tensor-core tile of 128).
  *   q            device fp16 [n_tokens][num_q_heads][head_dim], 16-byte aligned: the new tokens
  *                of all requests, packed
  *   token_offsets device int32 [batch + 1], not decreasing, in [0, n_tokens]: request b's
@@ -379,8 +381,6 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  *   k_codes .. page_table, max_pages   as for kvq_decode_attn
  *   seq_lens     device int32 [batch]: positions of each sequence, the new tokens included, in
  *                [0, min(max_seq_len, max_pages*page_size)]
- *                (For a batch of single tokens kvq_decode_attn is the faster call: here every
- *                request's rows take a tensor-core tile of 128.)
  *   causal       1: token i of request b sees the positions 0 .. seq_lens[b] - n_b + i;
  *                0: every position.  A token that sees none gets zeros.
  *   sm_scale     score scale, finite, of any sign
