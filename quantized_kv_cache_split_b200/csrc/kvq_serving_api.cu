@@ -32,6 +32,19 @@ bool needs_merge(const kvq_cache_desc* desc, const RowsPlan& p) {
   return p.splits > 1 || desc->fmt == KVQ_FMT_LUT4;
 }
 
+// How prompt attention is cut.  Up to 512 positions in one piece, written to the output directly:
+// the merge costs more than the split saves (512 positions, 200 tokens of 32 heads: 20.7 us against
+// 24.8; at 1024 positions the split wins, 22.8 against 25.6 for 64 tokens).  lut4 output goes
+// through the merge in any case and keeps its splits.
+RowsPlan plan_prompt(const kvq_cache_desc* desc, int n_tokens, int num_q_heads, int batch, int max_seq_len) {
+  RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len, kTargetCtas);
+  if (max_seq_len <= 4 * kKvTile && desc->fmt != KVQ_FMT_LUT4) {
+    p.splits = 1;
+    p.min_chunk = 4 * kKvTile;
+  }
+  return p;
+}
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The two parts of prefix decode: how each is cut.  Blocks of either fill an SM, so the prefix gets
@@ -113,7 +126,7 @@ int kvq_plan_step(int32_t batch, int32_t page_size, int32_t num_pages, int32_t m
 size_t kvq_prompt_workspace_size(const kvq_cache_desc* desc, int32_t n_tokens, int32_t num_q_heads,
                                  int32_t batch, int32_t max_seq_len) {
   if (check_rows(desc, n_tokens, num_q_heads, batch, max_seq_len) != KVQ_OK) return 0;
-  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len, kTargetCtas);
+  const RowsPlan p = plan_prompt(desc, n_tokens, num_q_heads, batch, max_seq_len);
   return kWorkspaceHeader +
          (needs_merge(desc, p) ? rows_partial_bytes(n_tokens, num_q_heads, desc->head_dim, p.splits) : 0);
 }
@@ -148,7 +161,7 @@ int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
   if (workspace_bytes < kvq_prompt_workspace_size(desc, n_tokens, num_q_heads, batch, max_seq_len))
     return KVQ_ERR_WORKSPACE;
   if (batch == 0 || n_tokens == 0) return KVQ_OK;
-  const RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len, kTargetCtas);
+  const RowsPlan p = plan_prompt(desc, n_tokens, num_q_heads, batch, max_seq_len);
   const bool merge = needs_merge(desc, p);
   RowsArgs r{};
   const OwnArgs own{};
