@@ -391,8 +391,9 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  *   out          device [n_tokens][num_q_heads][head_dim] of out_type, 16-byte aligned
  *   out_type     KVQ_OUT_F32 or KVQ_OUT_F16 (one rounding of the fp32 result)
  * Roundings: K and V values to fp16 once dequantized (nvfp4: first the block scale times the
- * vector scale; lut4: the rotated query as well), the weights to fp16 for the product with V;
- * scores, softmax statistics and sums are fp32.  Results do not depend on timing: the same
+ * vector scale; lut4: the rotated query as well), the weights to fp16 for the product with V (as
+ * 2^7 times their share of a maximum or more: each is off by at most 2^-11 of itself or 2^-32 of
+ * the largest); scores, softmax statistics and sums are fp32.  Results do not depend on timing: the same
  * call gives the same bits.
  * Same limits as kvq_decode_attn (KVQ_MAX_GROUP, KVQ_MAX_BATCH); lengths up to 2^29.
  * Sequences whose length, offsets or pages are out of range set KVQ_FLAG_BAD_SEQLEN /

@@ -59,10 +59,12 @@ static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kFillWarps * kFillRegs + 4 * 
               "register pool");
 constexpr int kOwnWarps = 12, kOwnRegs = 136;  // blocks of own units: three warpgroups of five
 static_assert(32 * (kOwnWarps * kOwnRegs + (kThreads / 32 - kOwnWarps) * kMmaRegs) <= 96 * kThreads, "register pool");
-// weights are 2^(s - m + 1): fp16's normal range reaches 2^-15 below the maximum's weight, and a
-// maximum may grow 2^7 to 2^14 times before it has to be raised (with 7 bits, the ragged prompts
-// took 247 us instead of 236)
-constexpr float kWeightBits = 1.f;
+// Weights are 2^(s - m + 7).  fp16's smallest step is then 2^-31 of the maximum's weight, so that a
+// long tail of small weights is not lost to rounding (with one bit of headroom 64K positions 2^-26
+// below the maximum, 0.1 % of the sum, vanished from the product while the denominator counted
+// them), and its normal range reaches 2^-21 below.  A tile of equal scores sums to 2^14, half of
+// kSafeSum; a maximum may grow 2^1 to 2^8 times before it has to be raised.
+constexpr float kWeightBits = 7.f;
 constexpr float kSafeSum = 32768.f;  // a tile's weights summing to less are all inside fp16
 constexpr uint32_t kTmemColumns = 512;
 // q8_0 and nvfp4 values enter the products halved (their rounded code * scale can pass the
@@ -720,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
         const bool mask = __any_sync(0xffffffffu, lim < kKvTile);
         // No pass over the tile for its maximum: the weights are taken under the maximum that
         // was last raised, and their sum (which the denominator needs anyway) tells whether one
-        // may have outgrown fp16: below 2^15 none has.  A maximum 2^14 times the old one always
+        // may have outgrown fp16: below 2^15 none has.  A maximum 2^8 times the old one always
         // gets there, one that is not above it never does.  Then, and on a row's first
         // positions, the maximum is raised and the tile done again.
         bool raise = __any_sync(0xffffffffu, m == -INFINITY && lim > 0);

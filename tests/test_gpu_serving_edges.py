@@ -1,0 +1,91 @@
+"""The serving operators at the edges of their ranges, on the GPU against 64-bit definitions."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from tests.serving_helpers import Pool, check_close  # noqa: E402
+
+FMTS = ["q8_0", "q4_0", "lut4", "nvfp4"]
+
+
+def dev(x, dtype=np.int32):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=dtype)).cuda()
+
+
+def fill(pool, k, v):
+    """Write K and V [positions, 1, D] into slots 0 .. and read the cache's values back."""
+    pool.cache.write(dev(k, np.float16), dev(v, np.float16), dev(np.arange(len(k))))
+    torch.cuda.synchronize()
+    pool.k, pool.v = pool.values("k"), pool.values("v")
+
+
+# ------------------------------------------------------------------ small weights
+
+# Weights enter the product with V in fp16 as 2^7 times their share of the maximum: steps of
+# 2^-24, so each is off by at most 2^-25 / 2^7 = 2^-32 of the largest.  Pool.attend allows 2^-26
+# per position; here the difference is the point.
+STEP, POOL_STEP = 2.0 ** -32, 2.0 ** -26
+
+
+def one_strong_key(fmt, n):
+    """n positions: K 0 but for one key whose score is 26.3 binary orders above theirs, where V is
+    0; V 1 elsewhere.  The answer is what the many small weights sum to."""
+    D, gap = 64, 26.3
+    pool = Pool(fmt, D, 1, 64, -(-n // 64), seed=40)
+    k, v = np.zeros((n, 1, D), dtype=np.float16), np.ones((n, 1, D), dtype=np.float16)
+    k[100], v[100] = 1.0, 0.0
+    fill(pool, k, v)
+    # the key as the cache holds it, so that the gap is what it should be in every format
+    ones = np.ones((1, D))
+    if fmt == "lut4":
+        from oracle import quant as OQ
+        ones = OQ.rotate_f64(ones, pool.signs)
+    q1 = gap * math.log(2) * math.sqrt(D) / float(ones[0] @ pool.k[100, 0])
+    return pool, q1
+
+
+def tight(pool, q, n, half):
+    """Pool.attend's answer and bound, with the steps of the weights as they are."""
+    want, bound = pool.attend(q, np.arange(n), 1 / math.sqrt(pool.D))
+    v = np.abs(pool.v[:n]).max()
+    term = n * v * (math.sqrt(pool.D) if pool.fmt == "lut4" else 1.0)
+    if pool.fmt == "lut4":
+        # all small weights are equal and so is V: their rounding scales one vector, which is
+        # rotated back as a whole
+        from oracle import quant as OQ
+        v = np.abs(OQ.unrotate_f64(pool.v[0], pool.signs)).max()
+    bound = bound - term * POOL_STEP + n * v * STEP
+    # what a lost tail would change has to stand out
+    assert np.abs(want).min() > 1.5 * bound.max()
+    return want, bound
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_prompt_small_weights_are_not_lost(fmt):
+    # as many rows as keep a unit's positions in one piece; all rows are the same
+    n, tokens, G = 32000, 4800, 8
+    pool, q1 = one_strong_key(fmt, n)
+    q = np.full((tokens, G, 64), q1, dtype=np.float16)
+    out = pool.cache.prompt_attention(dev(q, np.float16), dev([0, tokens]), dev([n]), n, dev([np.arange(n // 64)]), n // 64,
+                                      causal=False)
+    want, bound = tight(pool, q[0], n, False)
+    for i in (0, 77, tokens - 1):
+        check_close(out[i].cpu().numpy(), want, bound, False)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_prefix_small_weights_are_not_lost(fmt):
+    # 1024 requests of 8 heads: 32 row tiles, four pieces of 8000 positions
+    n, B, G = 32000, 1024, 8
+    pool, q1 = one_strong_key(fmt, n)
+    q = np.full((B, G, 64), q1, dtype=np.float16)
+    out = pool.cache.prefix_attention(dev(q, np.float16), dev([np.arange(n // 64)]), dev([n]), n, dev([0] * B), 0,
+                                      dev([[0]] * B), 1)
+    want, bound = tight(pool, q[0], n, False)
+    for i in (0, 500, B - 1):
+        check_close(out[i].cpu().numpy(), want, bound, False)
