@@ -953,11 +953,12 @@ RowsPlan plan_rows(int num_kv_heads, int group, int n_tokens, int num_groups, in
   return p;
 }
 
-// A warp per split, as many splits as the device holds warps of own units, whole blocks.
+// A warp per split, as many splits as the device holds warps of own units, whole blocks; no
+// split is longer than a sequence (with more pairs than slots the even share is).
 int plan_own(int num_kv_heads, int batch, int max_seq_len, int* ctas) {
   const int64_t pairs = (int64_t)std::max(batch, 1) * num_kv_heads;
   const int64_t slots = (int64_t)kTargetCtas * kOwnWarps;
-  const int64_t l = (pairs * max_seq_len + slots - 1) / slots;
+  const int64_t l = std::min<int64_t>((pairs * max_seq_len + slots - 1) / slots, max_seq_len);
   const int split = (int)std::max<int64_t>((l + kTile - 1) / kTile * kTile, kTile);
   const int64_t units = pairs * ((max_seq_len + split - 1) / split);
   *ctas = (int)std::min<int64_t>((units + kOwnWarps - 1) / kOwnWarps, 0x7fffffff);
