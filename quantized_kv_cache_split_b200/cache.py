@@ -92,7 +92,11 @@ class QuantizedKVCache:
         sequence and KV head).  ``v_fetch``: how V rows reach the SM when tau > 0:
         "kept" (only the kept rows, after the skip test), "with_k" (every V tile with its
         K tile; skipped rows are left out of the contraction only) or "auto" (with_k);
-        the result is the same."""
+        the result is the same.  ``stream``: as for prompt_attention."""
+        other = _elsewhere(stream, self._index)
+        if other is not None:
+            return _run_on(other, self._index, out, self.attention, q, seq_lens, max_seq_len, page_table, max_pages, tau,
+                           sm_scale, split_tokens, out, stats, max_scope, fused, v_fetch)
         scopes = {"split": 0, "cluster": kb.KVQ_OPT_SHARED_MAX, "sequence": kb.KVQ_OPT_GLOBAL_MAX}
         fetches = {"auto": 0, "kept": kb.KVQ_OPT_V_KEPT_ONLY, "with_k": kb.KVQ_OPT_V_WITH_K}
         if max_scope not in scopes:
@@ -115,8 +119,9 @@ class QuantizedKVCache:
         return out
 
     # ---------------------------------------------------------------- prompts, shared prefixes
-    def _rows_call(self, kind, size_fn, args, q, out, out_dtype, sm_scale, stream):
-        """Checks of q and out, the workspace, the output, the scale and the stream of a call."""
+    def _rows_call(self, kind, size_fn, args, q, out, out_dtype, sm_scale):
+        """Checks of q and out, the workspace, the output, the scale and the stream of a call on
+        torch's current stream."""
         D = self.head_dim
         if q.dim() != 3 or q.shape[2] != D:
             raise ValueError(f"q must be [tokens, heads, {D}], not {tuple(q.shape)}")
@@ -129,13 +134,11 @@ class QuantizedKVCache:
         if out_type is None:
             raise ValueError(f"the output is float32 or float16, not {out.dtype}")
         _want("out", out, out.dtype, self._index)
-        if stream is None:
-            stream = _raw_stream(self._index)
+        stream = _raw_stream(self._index)
         key = (kind,) + args
         nbytes = self._rows_bytes.get(key)
         if nbytes is None:
             nbytes = self._rows_bytes[key] = size_fn(self.desc, *args)
-        stream = kb._stream(stream)
         ws = self._ws_rows.get(stream)
         if ws is None or ws.numel() < nbytes:
             if ws is not None:
@@ -158,12 +161,20 @@ class QuantizedKVCache:
         padding and keep what ``out`` holds there.  Lengths, offsets and the table are int32
         tensors on the cache's GPU.
 
+        ``stream`` (a torch stream or a handle): launch there instead of on the current stream.
+        The inputs must be ready for it and stay alive until the call has run; a new output
+        belongs to that stream's memory, so wait for the stream before using it elsewhere.
+
         The workspace is kept per stream: calls on different streams may overlap, replays of
         graphs captured on one stream may not."""
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.prompt_attention(q, token_offsets, seq_lens, max_seq_len, page_table, max_pages, causal,
                                              sm_scale, out, out_dtype, stream)
+        other = _elsewhere(stream, self._index)
+        if other is not None:
+            return _run_on(other, self._index, out, self.prompt_attention, q, token_offsets, seq_lens, max_seq_len,
+                           page_table, max_pages, causal, sm_scale, out, out_dtype)
         B = seq_lens.numel()
         _want("seq_lens", seq_lens, torch.int32, self._index)
         _want("token_offsets", token_offsets, torch.int32, self._index, B + 1)
@@ -171,7 +182,7 @@ class QuantizedKVCache:
             _want("page_table", page_table, torch.int32, self._index, B * max_pages)
         n, Hq = q.shape[0], q.shape[1]
         ws, out, out_type, sm_scale, stream = self._rows_call("prompt", kb.kvq_prompt_workspace_size, (n, Hq, B, max_seq_len),
-                                                          q, out, out_dtype, sm_scale, stream)
+                                                          q, out, out_dtype, sm_scale)
         kb.kvq_prompt_attn(self.desc, q, n, Hq, self.k_codes, self.k_scales, self.v_codes, self.v_scales, page_table,
                            max_pages, seq_lens, max_seq_len, token_offsets, B, causal, sm_scale, ws, ws.numel(), out,
                            out_type, stream)
@@ -189,13 +200,17 @@ class QuantizedKVCache:
         one group of all) attends to the ``prefix_lens[g]`` positions of row g of
         ``prefix_table`` and each request to its own ``seq_lens[b]`` positions as well.  The
         prefix is read once per group, not once per request.  Lengths, offsets and tables are
-        int32 tensors on the cache's GPU.  The workspace is kept per stream (as for
-        prompt_attention)."""
+        int32 tensors on the cache's GPU.  ``stream`` and the workspace: as for prompt_attention."""
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.prefix_attention(q, prefix_table, prefix_lens, max_prefix_len, seq_lens, max_seq_len,
                                              page_table, max_pages, group_offsets, max_prefix_pages, sm_scale, out,
                                              out_dtype, stream)
+        other = _elsewhere(stream, self._index)
+        if other is not None:
+            return _run_on(other, self._index, out, self.prefix_attention, q, prefix_table, prefix_lens, max_prefix_len,
+                           seq_lens, max_seq_len, page_table, max_pages, group_offsets, max_prefix_pages, sm_scale, out,
+                           out_dtype)
         B, ng = q.shape[0], prefix_lens.numel()
         if max_prefix_pages is None:
             if prefix_table is None:
@@ -211,8 +226,7 @@ class QuantizedKVCache:
             _want("page_table", page_table, torch.int32, self._index, B * max_pages)
         Hq = q.shape[1]
         ws, out, out_type, sm_scale, stream = self._rows_call(
-            "prefix", kb.kvq_prefix_workspace_size, (B, Hq, ng, max_prefix_len, max_seq_len), q, out, out_dtype, sm_scale,
-            stream)
+            "prefix", kb.kvq_prefix_workspace_size, (B, Hq, ng, max_prefix_len, max_seq_len), q, out, out_dtype, sm_scale)
         kb.kvq_prefix_attn(self.desc, q, B, Hq, self.k_codes, self.k_scales, self.v_codes, self.v_scales, prefix_table,
                            max_prefix_pages, prefix_lens, max_prefix_len, group_offsets, ng, page_table, max_pages,
                            seq_lens, max_seq_len, sm_scale, ws, ws.numel(), out, out_type, stream)
@@ -247,6 +261,32 @@ def _cuda_index(device: torch.device) -> int:
 
 def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _elsewhere(stream, index: int):
+    """The torch stream of a call's ``stream`` argument when that is not the current one, else None."""
+    if stream is None:
+        return None
+    raw = kb._stream(stream)
+    if raw == 1:  # the legacy default stream's other name
+        raw = 0
+    if raw == _raw_stream(index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(raw, device=index) if raw else torch.cuda.default_stream(index)
+
+
+def _run_on(other, index: int, out, method, *args):
+    """method(*args) with ``other`` as the current stream, so that what it allocates is that
+    stream's memory: torch reuses a freed block in the order of the stream that it belongs to, and
+    of no other.  The current stream is expected to use a new output later on."""
+    here = torch.cuda.current_stream(index)
+    with torch.cuda.stream(other):
+        res = method(*args)
+    if out is None:
+        res.record_stream(here)
+    return res
 
 
 _OUT_TYPES = {torch.float32: kb.KVQ_OUT_F32, torch.float16: kb.KVQ_OUT_F16}

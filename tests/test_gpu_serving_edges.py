@@ -89,3 +89,42 @@ def test_prefix_small_weights_are_not_lost(fmt):
     want, bound = tight(pool, q[0], n, False)
     for i in (0, 500, B - 1):
         check_close(out[i].cpu().numpy(), want, bound, False)
+
+
+# ------------------------------------------------------------------ a stream given by its handle
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("op", ["prompt", "prefix", "decode"])
+def test_explicit_stream_takes_no_memory_of_another(op, raw):
+    """With stream=, the output and the workspace come from that stream's memory: a block that was
+    freed on the current one may still be in use there."""
+    pool = Pool("q4_0", 64, 1, 64, 40, seed=49)
+    q = dev(pool.queries(64, 8), np.float16)
+    tab, lens = dev([np.arange(40)]), dev([2500])
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if raw else side
+    many = dev([2500] * 64), dev(np.tile(np.arange(40), (64, 1)))
+    call = {"prompt": lambda **kw: pool.cache.prompt_attention(q, dev_off, lens, 2560, tab, 40, **kw),
+            "prefix": lambda **kw: pool.cache.prefix_attention(q, tab, lens, 2560, zero, 0, own, 1, **kw),
+            "decode": lambda **kw: pool.cache.attention(q, many[0], 2560, many[1], 40, tau=0.0, **kw)}[op]
+    dev_off, zero, own = dev([0, 64]), dev([0] * 64), dev([[0]] * 64)
+    want = call()
+    torch.cuda.synchronize()
+    fresh = Pool("q4_0", 64, 1, 64, 40, seed=49)
+    pool.cache, old = fresh.cache, pool.cache
+    # every block that the calls could want, freed on the current stream
+    sizes = [want.numel() * 4] + [t.numel() for t in (old._ws, *old._ws_rows.values()) if t is not None]
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    spans = [(b.data_ptr(), b.data_ptr() + b.numel()) for b in blocks]
+    del blocks
+    torch.cuda.synchronize()
+    out = call(stream=s)
+    side.synchronize()
+    mine = [out] + [t for t in (pool.cache._ws, *pool.cache._ws_rows.values()) if t is not None]
+    for t in mine:
+        assert not any(a < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < b for a, b in spans)
+    if op == "decode":   # its atomics' order may change the last bits
+        torch.testing.assert_close(out, want, rtol=0, atol=1e-5)
+    else:
+        assert torch.equal(out, want)
+    assert pool.cache.device_flags() == 0
