@@ -277,8 +277,8 @@ def kvq_noalloc_read_flags(stream=None) -> int:
 # kvq_plan_step, kvq_prompt_attn and kvq_prefix_attn take their many arguments as one block of
 # 64-bit words (ctypes converts arguments one by one, at a third of a microsecond each).
 _PLAN = struct.Struct("=18q")
-_PROMPT = struct.Struct("=15qd5q")
-_PREFIX = struct.Struct("=18qd5q")
+_PROMPT = struct.Struct("=15qd6q")
+_PREFIX = struct.Struct("=18qd6q")
 
 
 def _i32(x: int) -> int:
@@ -324,11 +324,13 @@ def kvq_prompt_attn(desc: KvqCacheDesc, q, n_tokens: int, num_q_heads: int, k_co
                     v_codes, v_scales, page_table, max_pages: int, seq_lens, max_seq_len: int,
                     token_offsets, batch: int, causal: bool, sm_scale: float, workspace,
                     workspace_bytes: int, out, out_type: int = KVQ_OUT_F32, stream=None,
-                    check: bool = True) -> int:
+                    check: bool = True, flags=None) -> int:
+    """flags: the device word (uint32) that fault bits are set in; None: the workspace's."""
     st = _lib.kvq_packed_call(1, _PROMPT.pack(
         ctypes.addressof(desc), _word(q), _i32(n_tokens), _i32(num_q_heads), _word(k_codes), _word(k_scales), _word(v_codes),
         _word(v_scales), _word(page_table), _i32(max_pages), _word(seq_lens), _i32(max_seq_len), _word(token_offsets),
-        _i32(batch), int(causal), sm_scale, _word(workspace), workspace_bytes, _word(out), out_type, _stream(stream) or 0))
+        _i32(batch), int(causal), sm_scale, _word(workspace), workspace_bytes, _word(out), out_type, _stream(stream) or 0,
+        _word(flags)))
     if check:
         _check("kvq_prompt_attn", st)
     return st
@@ -338,12 +340,14 @@ def kvq_prefix_attn(desc: KvqCacheDesc, q, batch: int, num_q_heads: int, k_codes
                     v_scales, prefix_table, max_prefix_pages: int, prefix_lens, max_prefix_len: int,
                     group_offsets, num_groups: int, page_table, max_pages: int, seq_lens,
                     max_seq_len: int, sm_scale: float, workspace, workspace_bytes: int, out,
-                    out_type: int = KVQ_OUT_F32, stream=None, check: bool = True) -> int:
+                    out_type: int = KVQ_OUT_F32, stream=None, check: bool = True, flags=None) -> int:
+    """flags: as for kvq_prompt_attn."""
     st = _lib.kvq_packed_call(2, _PREFIX.pack(
         ctypes.addressof(desc), _word(q), _i32(batch), _i32(num_q_heads), _word(k_codes), _word(k_scales), _word(v_codes),
         _word(v_scales), _word(prefix_table), _i32(max_prefix_pages), _word(prefix_lens), _i32(max_prefix_len),
         _word(group_offsets), _i32(num_groups), _word(page_table), _i32(max_pages), _word(seq_lens), _i32(max_seq_len),
-        sm_scale, _word(workspace), workspace_bytes, _word(out), out_type, _stream(stream) or 0))
+        sm_scale, _word(workspace), workspace_bytes, _word(out), out_type, _stream(stream) or 0,
+        _word(flags)))
     if check:
         _check("kvq_prefix_attn", st)
     return st

@@ -58,6 +58,8 @@ class QuantizedKVCache:
         self._ws_rows = {}       # prompt and prefix attention: a workspace per stream
         self._ws_old = []        # outgrown ones: a captured graph may still use them
         self._rows_bytes = {}    # workspace bytes by request shape
+        self._flags = torch.zeros(256, dtype=torch.uint8, device=self.device)  # their flag word
+        _settle(self.device)
 
     # ---------------------------------------------------------------- writes
     def write(self, k: torch.Tensor, v: torch.Tensor, slots: Optional[torch.Tensor] = None,
@@ -139,12 +141,15 @@ class QuantizedKVCache:
         nbytes = self._rows_bytes.get(key)
         if nbytes is None:
             nbytes = self._rows_bytes[key] = size_fn(self.desc, *args)
-        ws = self._ws_rows.get(stream)
-        if ws is None or ws.numel() < nbytes:
-            if ws is not None:
-                self._ws_old.append(ws)
-            ws = self._ws_rows[stream] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-            kb.kvq_workspace_init(ws, ws.numel(), stream)
+        if torch._C._cuda_isCurrentStreamCapturing():
+            # the graph's own memory: no other graph and no later call uses it
+            ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        else:
+            ws = self._ws_rows.get(stream)
+            if ws is None or ws.numel() < nbytes:
+                if ws is not None:
+                    self._ws_old.append(ws)
+                ws = self._ws_rows[stream] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         return ws, out, out_type, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale, stream
 
     def prompt_attention(self, q: torch.Tensor, token_offsets: torch.Tensor, seq_lens: torch.Tensor,
@@ -165,8 +170,8 @@ class QuantizedKVCache:
         The inputs must be ready for it and stay alive until the call has run; a new output
         belongs to that stream's memory, so wait for the stream before using it elsewhere.
 
-        The workspace is kept per stream: calls on different streams may overlap, replays of
-        graphs captured on one stream may not."""
+        The workspace is kept per stream, and a captured call has one of its own in its graph's
+        memory: calls on different streams and replays of different graphs may overlap."""
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.prompt_attention(q, token_offsets, seq_lens, max_seq_len, page_table, max_pages, causal,
@@ -185,7 +190,7 @@ class QuantizedKVCache:
                                                           q, out, out_dtype, sm_scale)
         kb.kvq_prompt_attn(self.desc, q, n, Hq, self.k_codes, self.k_scales, self.v_codes, self.v_scales, page_table,
                            max_pages, seq_lens, max_seq_len, token_offsets, B, causal, sm_scale, ws, ws.numel(), out,
-                           out_type, stream)
+                           out_type, stream, flags=self._flags)
         return out
 
     def prefix_attention(self, q: torch.Tensor, prefix_table: Optional[torch.Tensor],
@@ -229,17 +234,15 @@ class QuantizedKVCache:
             "prefix", kb.kvq_prefix_workspace_size, (B, Hq, ng, max_prefix_len, max_seq_len), q, out, out_dtype, sm_scale)
         kb.kvq_prefix_attn(self.desc, q, B, Hq, self.k_codes, self.k_scales, self.v_codes, self.v_scales, prefix_table,
                            max_prefix_pages, prefix_lens, max_prefix_len, group_offsets, ng, page_table, max_pages,
-                           seq_lens, max_seq_len, sm_scale, ws, ws.numel(), out, out_type, stream)
+                           seq_lens, max_seq_len, sm_scale, ws, ws.numel(), out, out_type, stream,
+                           flags=self._flags)
         return out
 
     def device_flags(self) -> int:
-        """KVQ_FLAG_* bits of the calls so far."""
-        flags = 0 if self._ws is None else kb.kvq_read_device_flags(self._ws)
-        if self._ws_rows:
-            torch.cuda.synchronize(self._index)  # their streams
-            for ws in (*self._ws_rows.values(), *self._ws_old):
-                flags |= kb.kvq_read_device_flags(ws)
-        return flags
+        """KVQ_FLAG_* bits of the calls so far, replays of captured ones among them."""
+        torch.cuda.synchronize(self._index)  # their streams
+        flags = kb.kvq_read_device_flags(self._flags)
+        return flags if self._ws is None else flags | kb.kvq_read_device_flags(self._ws)
 
 
 def _want(name: str, t: torch.Tensor, dtype: torch.dtype, index: int, numel: Optional[int] = None) -> None:
@@ -257,6 +260,12 @@ def _cuda_index(device: torch.device) -> int:
     if device.type != "cuda":
         return -1
     return torch.cuda.current_device() if device.index is None else device.index
+
+
+def _settle(device: torch.device) -> None:
+    """Wait until buffers just made hold their first values: their first use may be on any stream."""
+    if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
 
 
 def _raw_stream(index: int) -> int:
@@ -310,6 +319,7 @@ class PagePlanner:
         self.seq_lens, self.token_offsets, self.free_count = ints(batch), ints(batch + 1), ints(1)
         self.slots, self.positions = ints(max_tokens), ints(max_tokens)
         self._ws = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        _settle(self.device)
 
     def step(self, new_lens: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
              free_pages: torch.Tensor, free_count: torch.Tensor, stream=None) -> None:

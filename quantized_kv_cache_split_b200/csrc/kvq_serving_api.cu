@@ -79,6 +79,135 @@ void set_partials(RowsArgs* r, uint8_t* at) {
   r->part_l = r->part_m + n;
 }
 
+// The calls of the same names; flags: the device flag word, null for the workspace's.
+int prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
+                int32_t num_q_heads, const void* k_codes, const void* k_scales,
+                const void* v_codes, const void* v_scales, const int32_t* page_table,
+                int32_t max_pages, const int32_t* seq_lens, int32_t max_seq_len,
+                const int32_t* token_offsets, int32_t batch, int32_t causal, float sm_scale,
+                void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
+                uint32_t* flags, void* stream) {
+  int st = check_rows(desc, n_tokens, num_q_heads, batch, max_seq_len);
+  if (st != KVQ_OK) return st;
+  if (max_pages < 1 || (causal != 0 && causal != 1) || (out_type != KVQ_OUT_F32 && out_type != KVQ_OUT_F16) ||
+      !isfinite(sm_scale))
+    return KVQ_ERR_INVALID_ARG;
+  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !seq_lens || !token_offsets || !workspace || !out)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
+      !aligned16(workspace) || !aligned16(out) || (reinterpret_cast<uintptr_t>(flags) & 3u))
+    return KVQ_ERR_INVALID_ARG;
+  if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
+  if (workspace_bytes < kvq_prompt_workspace_size(desc, n_tokens, num_q_heads, batch, max_seq_len))
+    return KVQ_ERR_WORKSPACE;
+  if (batch == 0 || n_tokens == 0) return KVQ_OK;
+  const RowsPlan p = plan_prompt(desc, n_tokens, num_q_heads, batch, max_seq_len);
+  const bool merge = needs_merge(desc, p);
+  RowsArgs r{};
+  const OwnArgs own{};
+  r.desc = *desc;
+  r.q = q;
+  r.n_tokens = n_tokens;
+  r.num_q_heads = num_q_heads;
+  r.group = num_q_heads / desc->num_kv_heads;
+  r.k_codes = k_codes;
+  r.k_scales = k_scales;
+  r.v_codes = v_codes;
+  r.v_scales = v_scales;
+  r.table = page_table;
+  r.max_pages = max_pages;
+  r.lens = seq_lens;
+  r.max_len = max_seq_len;
+  r.offsets = token_offsets;
+  r.num_groups = batch;
+  r.causal = causal;
+  r.sm_scale = sm_scale;
+  r.splits = p.splits;
+  r.min_chunk = p.min_chunk;
+  r.ctas = p.ctas;
+  r.chunk_out = static_cast<int32_t*>(workspace) + kChunkWord;
+  r.row_tiles = p.row_tiles;
+  r.flags = flags ? flags : static_cast<uint32_t*>(workspace);
+  if (merge) set_partials(&r, static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
+  else r.out = out;
+  r.out_f16 = out_type == KVQ_OUT_F16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = launch_rows(r, own, s);
+  if (st != KVQ_OK || !merge) return st;
+  return launch_rows_merge(r, own, out, r.out_f16, s);
+}
+
+int prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_t num_q_heads,
+                const void* k_codes, const void* k_scales, const void* v_codes,
+                const void* v_scales, const int32_t* prefix_table, int32_t max_prefix_pages,
+                const int32_t* prefix_lens, int32_t max_prefix_len,
+                const int32_t* group_offsets, int32_t num_groups, const int32_t* page_table,
+                int32_t max_pages, const int32_t* seq_lens, int32_t max_seq_len, float sm_scale,
+                void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
+                uint32_t* flags, void* stream) {
+  int st = check_rows(desc, batch, num_q_heads, num_groups, max_prefix_len);
+  if (st != KVQ_OK) return st;
+  if (max_prefix_pages < 1 || max_pages < 1 || max_seq_len < 0 || num_groups < 1 ||
+      (out_type != KVQ_OUT_F32 && out_type != KVQ_OUT_F16) || !isfinite(sm_scale))
+    return KVQ_ERR_INVALID_ARG;
+  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !prefix_lens || !seq_lens || !workspace || !out)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
+      !aligned16(workspace) || !aligned16(out) || (reinterpret_cast<uintptr_t>(flags) & 3u))
+    return KVQ_ERR_INVALID_ARG;
+  if (!group_offsets && num_groups != 1) return KVQ_ERR_INVALID_ARG;
+  if (!prefix_table && (int64_t)num_groups * max_prefix_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
+  if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
+  if (batch > KVQ_MAX_BATCH || max_seq_len > kMaxLen) return KVQ_ERR_UNSUPPORTED;
+  if (workspace_bytes < kvq_prefix_workspace_size(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len))
+    return KVQ_ERR_WORKSPACE;
+  if (batch == 0) return KVQ_OK;
+  const PrefixPlan p = plan_prefix(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  RowsArgs r{};
+  r.desc = *desc;
+  r.q = q;
+  r.n_tokens = batch;
+  r.num_q_heads = num_q_heads;
+  r.group = num_q_heads / desc->num_kv_heads;
+  r.k_codes = k_codes;
+  r.k_scales = k_scales;
+  r.v_codes = v_codes;
+  r.v_scales = v_scales;
+  r.table = prefix_table;
+  r.max_pages = max_prefix_pages;
+  r.lens = prefix_lens;
+  r.max_len = max_prefix_len;
+  r.offsets = group_offsets;
+  r.num_groups = num_groups;
+  r.causal = 0;
+  r.sm_scale = sm_scale;
+  r.splits = p.rows.splits;
+  r.min_chunk = p.rows.min_chunk;
+  r.ctas = p.rows.ctas;
+  r.chunk_out = static_cast<int32_t*>(workspace) + kChunkWord;
+  r.row_tiles = max_prefix_len > 0 ? p.rows.row_tiles : 0;
+  r.flags = flags ? flags : reinterpret_cast<uint32_t*>(ws);
+  set_partials(&r, ws + kWorkspaceHeader);
+  OwnArgs own{};
+  own.max_splits = p.own_splits;
+  own.units = (int64_t)batch * desc->num_kv_heads * p.own_splits;
+  own.table = page_table;
+  own.max_pages = max_pages;
+  own.seq_lens = seq_lens;
+  own.max_seq_len = max_seq_len;
+  own.split = p.own_split;
+  const size_t n_own = (size_t)batch * num_q_heads * p.own_splits;
+  own.part_o = reinterpret_cast<float*>(
+      ws + kWorkspaceHeader + round256(rows_partial_bytes(batch, num_q_heads, desc->head_dim, p.rows.splits)));
+  own.part_m = own.part_o + n_own * desc->head_dim;
+  own.part_l = own.part_m + n_own;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = launch_rows(r, own, s);
+  if (st != KVQ_OK) return st;
+  return launch_rows_merge(r, own, out, out_type == KVQ_OUT_F16, s);
+}
+
 }  // namespace
 }  // namespace kvq
 
@@ -147,54 +276,9 @@ int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
                     const int32_t* token_offsets, int32_t batch, int32_t causal, float sm_scale,
                     void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
                     void* stream) {
-  int st = check_rows(desc, n_tokens, num_q_heads, batch, max_seq_len);
-  if (st != KVQ_OK) return st;
-  if (max_pages < 1 || (causal != 0 && causal != 1) || (out_type != KVQ_OUT_F32 && out_type != KVQ_OUT_F16) ||
-      !isfinite(sm_scale))
-    return KVQ_ERR_INVALID_ARG;
-  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !seq_lens || !token_offsets || !workspace || !out)
-    return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
-      !aligned16(workspace) || !aligned16(out))
-    return KVQ_ERR_INVALID_ARG;
-  if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
-  if (workspace_bytes < kvq_prompt_workspace_size(desc, n_tokens, num_q_heads, batch, max_seq_len))
-    return KVQ_ERR_WORKSPACE;
-  if (batch == 0 || n_tokens == 0) return KVQ_OK;
-  const RowsPlan p = plan_prompt(desc, n_tokens, num_q_heads, batch, max_seq_len);
-  const bool merge = needs_merge(desc, p);
-  RowsArgs r{};
-  const OwnArgs own{};
-  r.desc = *desc;
-  r.q = q;
-  r.n_tokens = n_tokens;
-  r.num_q_heads = num_q_heads;
-  r.group = num_q_heads / desc->num_kv_heads;
-  r.k_codes = k_codes;
-  r.k_scales = k_scales;
-  r.v_codes = v_codes;
-  r.v_scales = v_scales;
-  r.table = page_table;
-  r.max_pages = max_pages;
-  r.lens = seq_lens;
-  r.max_len = max_seq_len;
-  r.offsets = token_offsets;
-  r.num_groups = batch;
-  r.causal = causal;
-  r.sm_scale = sm_scale;
-  r.splits = p.splits;
-  r.min_chunk = p.min_chunk;
-  r.ctas = p.ctas;
-  r.chunk_out = static_cast<int32_t*>(workspace) + kChunkWord;
-  r.row_tiles = p.row_tiles;
-  r.flags = static_cast<uint32_t*>(workspace);
-  if (merge) set_partials(&r, static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
-  else r.out = out;
-  r.out_f16 = out_type == KVQ_OUT_F16;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = launch_rows(r, own, s);
-  if (st != KVQ_OK || !merge) return st;
-  return launch_rows_merge(r, own, out, r.out_f16, s);
+  return prompt_attn(desc, q, n_tokens, num_q_heads, k_codes, k_scales, v_codes, v_scales, page_table, max_pages, seq_lens,
+                     max_seq_len, token_offsets, batch, causal, sm_scale, workspace, workspace_bytes, out, out_type,
+                     nullptr, stream);
 }
 
 int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_t num_q_heads,
@@ -205,71 +289,14 @@ int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, in
                     int32_t max_pages, const int32_t* seq_lens, int32_t max_seq_len, float sm_scale,
                     void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
                     void* stream) {
-  int st = check_rows(desc, batch, num_q_heads, num_groups, max_prefix_len);
-  if (st != KVQ_OK) return st;
-  if (max_prefix_pages < 1 || max_pages < 1 || max_seq_len < 0 || num_groups < 1 ||
-      (out_type != KVQ_OUT_F32 && out_type != KVQ_OUT_F16) || !isfinite(sm_scale))
-    return KVQ_ERR_INVALID_ARG;
-  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !prefix_lens || !seq_lens || !workspace || !out)
-    return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
-      !aligned16(workspace) || !aligned16(out))
-    return KVQ_ERR_INVALID_ARG;
-  if (!group_offsets && num_groups != 1) return KVQ_ERR_INVALID_ARG;
-  if (!prefix_table && (int64_t)num_groups * max_prefix_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
-  if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
-  if (batch > KVQ_MAX_BATCH || max_seq_len > kMaxLen) return KVQ_ERR_UNSUPPORTED;
-  if (workspace_bytes < kvq_prefix_workspace_size(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len))
-    return KVQ_ERR_WORKSPACE;
-  if (batch == 0) return KVQ_OK;
-  const PrefixPlan p = plan_prefix(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  RowsArgs r{};
-  r.desc = *desc;
-  r.q = q;
-  r.n_tokens = batch;
-  r.num_q_heads = num_q_heads;
-  r.group = num_q_heads / desc->num_kv_heads;
-  r.k_codes = k_codes;
-  r.k_scales = k_scales;
-  r.v_codes = v_codes;
-  r.v_scales = v_scales;
-  r.table = prefix_table;
-  r.max_pages = max_prefix_pages;
-  r.lens = prefix_lens;
-  r.max_len = max_prefix_len;
-  r.offsets = group_offsets;
-  r.num_groups = num_groups;
-  r.causal = 0;
-  r.sm_scale = sm_scale;
-  r.splits = p.rows.splits;
-  r.min_chunk = p.rows.min_chunk;
-  r.ctas = p.rows.ctas;
-  r.chunk_out = static_cast<int32_t*>(workspace) + kChunkWord;
-  r.row_tiles = max_prefix_len > 0 ? p.rows.row_tiles : 0;
-  r.flags = reinterpret_cast<uint32_t*>(ws);
-  set_partials(&r, ws + kWorkspaceHeader);
-  OwnArgs own{};
-  own.max_splits = p.own_splits;
-  own.units = (int64_t)batch * desc->num_kv_heads * p.own_splits;
-  own.table = page_table;
-  own.max_pages = max_pages;
-  own.seq_lens = seq_lens;
-  own.max_seq_len = max_seq_len;
-  own.split = p.own_split;
-  const size_t n_own = (size_t)batch * num_q_heads * p.own_splits;
-  own.part_o = reinterpret_cast<float*>(
-      ws + kWorkspaceHeader + round256(rows_partial_bytes(batch, num_q_heads, desc->head_dim, p.rows.splits)));
-  own.part_m = own.part_o + n_own * desc->head_dim;
-  own.part_l = own.part_m + n_own;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = launch_rows(r, own, s);
-  if (st != KVQ_OK) return st;
-  return launch_rows_merge(r, own, out, out_type == KVQ_OUT_F16, s);
+  return prefix_attn(desc, q, batch, num_q_heads, k_codes, k_scales, v_codes, v_scales, prefix_table, max_prefix_pages,
+                     prefix_lens, max_prefix_len, group_offsets, num_groups, page_table, max_pages, seq_lens, max_seq_len,
+                     sm_scale, workspace, workspace_bytes, out, out_type, nullptr, stream);
 }
 
 // The three calls above from one block of 64-bit words, in their arguments' order (pointers and
 // integers as they are, a float as a double's bits): for bindings whose cost per argument counts.
+// The attention calls take one word more at the end: the device flag word, 0 for the workspace's.
 int kvq_packed_call(int32_t which, const int64_t* w) {
   if (!w) return KVQ_ERR_INVALID_ARG;
   auto ptr = [&](int i) { return reinterpret_cast<void*>(static_cast<uintptr_t>(w[i])); };
@@ -286,13 +313,13 @@ int kvq_packed_call(int32_t which, const int64_t* w) {
       return kvq_plan_step(num(0), num(1), num(2), num(3), num(4), ints(5), ints(6), ints(7), ints(8), ints(9), ints(10),
                            ints(11), ints(12), ints(13), ints(14), ptr(15), (size_t)w[16], ptr(17));
     case 1:
-      return kvq_prompt_attn(desc, ptr(1), num(2), num(3), ptr(4), ptr(5), ptr(6), ptr(7), ints(8), num(9), ints(10),
-                             num(11), ints(12), num(13), num(14), real(15), ptr(16), (size_t)w[17], ptr(18), num(19),
-                             ptr(20));
+      return prompt_attn(desc, ptr(1), num(2), num(3), ptr(4), ptr(5), ptr(6), ptr(7), ints(8), num(9), ints(10),
+                         num(11), ints(12), num(13), num(14), real(15), ptr(16), (size_t)w[17], ptr(18), num(19),
+                         static_cast<uint32_t*>(ptr(21)), ptr(20));
     case 2:
-      return kvq_prefix_attn(desc, ptr(1), num(2), num(3), ptr(4), ptr(5), ptr(6), ptr(7), ints(8), num(9), ints(10),
-                             num(11), ints(12), num(13), ints(14), num(15), ints(16), num(17), real(18), ptr(19),
-                             (size_t)w[20], ptr(21), num(22), ptr(23));
+      return prefix_attn(desc, ptr(1), num(2), num(3), ptr(4), ptr(5), ptr(6), ptr(7), ints(8), num(9), ints(10),
+                         num(11), ints(12), num(13), ints(14), num(15), ints(16), num(17), real(18), ptr(19),
+                         (size_t)w[20], ptr(21), num(22), static_cast<uint32_t*>(ptr(24)), ptr(23));
     default:
       return KVQ_ERR_INVALID_ARG;
   }

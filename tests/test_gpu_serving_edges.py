@@ -128,3 +128,79 @@ def test_explicit_stream_takes_no_memory_of_another(op, raw):
     else:
         assert torch.equal(out, want)
     assert pool.cache.device_flags() == 0
+
+
+# ------------------------------------------------------------------ captured calls
+
+def test_flags_of_captured_calls():
+    """Warm-up on one stream, capture on torch's own: the flags of every replay stay until they
+    are read, in the first graph and in a second one."""
+    import quantized_kv_cache_split_b200 as K
+    pool = Pool("q8_0", 64, 1, 64, 10, seed=45)
+    q, lens = dev(pool.queries(4, 4), np.float16), dev([600])
+    off, table = dev([0, 4]), dev([np.arange(10)])
+    out = torch.zeros(4, 4, 64, device="cuda")
+    call = lambda: pool.cache.prompt_attention(q, off, lens, 640, table, 10, out=out)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    want = out.clone()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            call()
+    assert pool.cache.device_flags() == 0
+    for g in reversed(graphs):                                  # the second before the first
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want) and pool.cache.device_flags() == 0
+    lens.fill_(-1)
+    graphs[1].replay()
+    lens.fill_(600)
+    for g in graphs:                                            # clean replays do not hide it
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    assert pool.cache.device_flags() == K.KVQ_FLAG_BAD_SEQLEN
+
+
+def test_captured_calls_have_their_own_workspace():
+    """Graphs replayed at once on two streams, beside eager calls on a third that need a larger
+    workspace: each gives what it gives alone."""
+    pool = Pool("q4_0", 64, 1, 64, 60, seed=46)
+    table = dev([np.arange(60)])
+    qs = [dev(pool.queries(n, 8), np.float16) for n in (3, 5, 90)]
+    outs = [torch.zeros(q.shape, device="cuda") for q in qs]
+    lens = [dev([n]) for n in (3800, 3000, 2500)]
+    offs = [dev([0, q.shape[0]]) for q in qs]
+    call = lambda i: pool.cache.prompt_attention(qs[i], offs[i], lens[i], 3840, table, 60, out=outs[i])  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for i in range(2):
+            call(i)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs[:2]]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g, stream=side):
+            call(i)
+    with torch.cuda.stream(side):
+        call(2)
+    torch.cuda.synchronize()
+    want.append(outs[2].clone())
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(side):
+            call(2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert pool.cache.device_flags() == 0

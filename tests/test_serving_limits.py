@@ -29,3 +29,13 @@ def test_prefix_workspace_holds_a_partial_of_both_parts(batch, hkv):
                 # least, and no more splits than there are SMs, and warps on them
                 assert size >= 256 + 2 * partials(rows, 1, 128), (fmt, prefix, own)
                 assert size <= 512 + partials(rows, 148 + 148 * 12 // (batch * hkv) + 1, 128), (fmt, prefix, own)
+
+
+# ------------------------------------------------------------------ a flag word outside the workspace
+
+def test_flag_words_must_be_aligned():
+    for flags in (FAKE + 1, FAKE + 2):
+        assert K.kvq_prompt_attn(desc(), FAKE, 8, 16, FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, 256, FAKE, 2, 1, 0.1, FAKE,
+                                 1 << 40, FAKE, stream=0, check=False, flags=flags) == K.KVQ_ERR_INVALID_ARG
+        assert K.kvq_prefix_attn(desc(), FAKE, 8, 16, FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, 256, FAKE, 2, FAKE, 2, FAKE,
+                                 128, 0.1, FAKE, 1 << 40, FAKE, stream=0, check=False, flags=flags) == K.KVQ_ERR_INVALID_ARG
