@@ -347,7 +347,8 @@ int kvq_noalloc_read_flags(uint32_t* flags, void* stream);
  * KVQ_FLAG_BAD_PAGE: a page id outside [0, num_pages) among the pages that the step moves or
  * continues, or a count that does not fit the pool; KVQ_FLAG_NO_PAGES; KVQ_FLAG_NO_SLOTS),
  * returns seq_lens and the count as they were, zero offsets and -1 slots.
- * Apart from the two pairs named above the buffers must not overlap.  batch == 0 is a no-op.
+ * Apart from the two pairs named above the buffers must not overlap.  batch == 0 is a no-op
+ * (slots and all else stay as they were).
  */
 int kvq_plan_step(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages,
                   int32_t max_tokens, const int32_t* seq_lens, const int32_t* new_lens,
@@ -378,6 +379,7 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  *                tokens are rows token_offsets[b] .. token_offsets[b+1] - 1, the last ones of
  *                its sequence (n_b = their number, possibly 0).  Rows of q outside every
  *                request are padding: not read, and their output rows are left as they were.
+ *                n_tokens == 0 or batch == 0: nothing is done, and the buffers may be null.
  *   k_codes .. page_table, max_pages   as for kvq_decode_attn
  *   seq_lens     device int32 [batch]: positions of each sequence, the new tokens included, in
  *                [0, min(max_seq_len, max_pages*page_size)]
@@ -425,7 +427,8 @@ int kvq_prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
  *   other arguments as for kvq_prompt_attn; the workspace is kvq_prefix_workspace_size(...)
  * The requests' own positions are meant to be the shorter part (a warp per request, KV head and
  * split); K there is not rounded to fp16 for q8_0, q4_0 and lut4.
- * A request without any position gets zeros.
+ * A request without any position gets zeros.  batch == 0: nothing is done, and the buffers may be
+ * null.
  */
 int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_t num_q_heads,
                     const void* k_codes, const void* k_scales, const void* v_codes,

@@ -317,7 +317,7 @@ class PagePlanner:
         self._index = _cuda_index(self.device)
         ints = lambda n: torch.zeros(n, dtype=torch.int32, device=self.device)  # noqa: E731
         self.seq_lens, self.token_offsets, self.free_count = ints(batch), ints(batch + 1), ints(1)
-        self.slots, self.positions = ints(max_tokens), ints(max_tokens)
+        self.slots, self.positions = ints(max_tokens).fill_(-1), ints(max_tokens)
         self._ws = torch.zeros(256, dtype=torch.uint8, device=self.device)
         _settle(self.device)
 

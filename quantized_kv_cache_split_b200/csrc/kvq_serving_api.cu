@@ -92,6 +92,7 @@ int prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
   if (max_pages < 1 || (causal != 0 && causal != 1) || (out_type != KVQ_OUT_F32 && out_type != KVQ_OUT_F16) ||
       !isfinite(sm_scale))
     return KVQ_ERR_INVALID_ARG;
+  if (batch == 0 || n_tokens == 0) return KVQ_OK;  // (buffers of no elements may be null)
   if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !seq_lens || !token_offsets || !workspace || !out)
     return KVQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
@@ -100,7 +101,6 @@ int prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
   if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
   if (workspace_bytes < kvq_prompt_workspace_size(desc, n_tokens, num_q_heads, batch, max_seq_len))
     return KVQ_ERR_WORKSPACE;
-  if (batch == 0 || n_tokens == 0) return KVQ_OK;
   const RowsPlan p = plan_prompt(desc, n_tokens, num_q_heads, batch, max_seq_len);
   const bool merge = needs_merge(desc, p);
   RowsArgs r{};
@@ -150,6 +150,8 @@ int prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_
   if (max_prefix_pages < 1 || max_pages < 1 || max_seq_len < 0 || num_groups < 1 ||
       (out_type != KVQ_OUT_F32 && out_type != KVQ_OUT_F16) || !isfinite(sm_scale))
     return KVQ_ERR_INVALID_ARG;
+  if (batch > KVQ_MAX_BATCH || max_seq_len > kMaxLen) return KVQ_ERR_UNSUPPORTED;
+  if (batch == 0) return KVQ_OK;  // (buffers of no elements may be null)
   if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !prefix_lens || !seq_lens || !workspace || !out)
     return KVQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) || !aligned16(v_scales) ||
@@ -158,10 +160,8 @@ int prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_
   if (!group_offsets && num_groups != 1) return KVQ_ERR_INVALID_ARG;
   if (!prefix_table && (int64_t)num_groups * max_prefix_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
   if (!page_table && (int64_t)batch * max_pages > desc->num_pages) return KVQ_ERR_INVALID_ARG;
-  if (batch > KVQ_MAX_BATCH || max_seq_len > kMaxLen) return KVQ_ERR_UNSUPPORTED;
   if (workspace_bytes < kvq_prefix_workspace_size(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len))
     return KVQ_ERR_WORKSPACE;
-  if (batch == 0) return KVQ_OK;
   const PrefixPlan p = plan_prefix(desc, batch, num_q_heads, num_groups, max_prefix_len, max_seq_len);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   RowsArgs r{};
@@ -226,12 +226,12 @@ int kvq_plan_step(int32_t batch, int32_t page_size, int32_t num_pages, int32_t m
   if (batch > KVQ_MAX_BATCH || (int64_t)num_pages * page_size > 0x7fffffffLL ||
       (int64_t)max_pages * page_size > 0x7fffffffLL)
     return KVQ_ERR_UNSUPPORTED;
+  if (batch == 0) return KVQ_OK;  // (buffers of no elements may be null)
   if (!seq_lens || !new_lens || !free_pages || !free_count || !page_table || !seq_lens_out || !free_count_out ||
       !token_offsets || (!slots && max_tokens > 0) || !workspace)
     return KVQ_ERR_INVALID_ARG;
   if (!aligned16(slots) || !aligned16(positions) || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
   if (workspace_bytes < kWorkspaceHeader) return KVQ_ERR_WORKSPACE;
-  if (batch == 0) return KVQ_OK;
   PlanArgs a;
   a.batch = batch;
   a.page_size = page_size;

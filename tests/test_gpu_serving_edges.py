@@ -204,3 +204,27 @@ def test_captured_calls_have_their_own_workspace():
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
     assert pool.cache.device_flags() == 0
+
+
+# ------------------------------------------------------------------ calls without work
+
+def test_calls_without_work():
+    import quantized_kv_cache_split_b200 as K
+    pool = Pool("q4_0", 64, 2, 64, 4, seed=44)
+    c, none = pool.cache, torch.zeros(0, dtype=torch.int32, device="cuda")
+    q0 = torch.zeros(0, 4, 64, dtype=torch.float16, device="cuda")
+    table = dev([[0, 1], [2, 3]])
+    assert c.prompt_attention(q0, dev([0, 0, 0]), dev([100, 5]), 128, table, 2).shape == (0, 4, 64)     # no new tokens
+    assert c.prompt_attention(q0, dev([0]), none, 128, none.view(0, 2), 2).shape == (0, 4, 64)          # no requests
+    pad = torch.full((3, 4, 64), 2.0, device="cuda")
+    c.prompt_attention(dev(pool.queries(3, 4), np.float16), dev([0]), none, 128, none.view(0, 2), 2, out=pad)
+    assert (pad == 2.0).all()                                                                           # padding alone
+    assert c.prefix_attention(q0, dev([[0, 1]]), dev([100]), 128, none, 64, none.view(0, 2), 2).shape == (0, 4, 64)
+    p = K.PagePlanner(0, 64, 4, 2, 8)
+    assert (p.slots == -1).all()                                  # before a step nothing has a slot
+    p.step(none, none.view(0, 2), p.seq_lens, dev([0, 1, 2, 3]), p.free_count)
+    assert (p.slots == -1).all()
+    p = K.PagePlanner(2, 64, 4, 2, 0)                             # room for no token
+    p.free_count.fill_(4)
+    p.step(dev([0, 0]), table, p.seq_lens, dev([0, 1, 2, 3]), p.free_count)
+    assert p.device_flags() == 0 and c.device_flags() == 0

@@ -39,3 +39,20 @@ def test_flag_words_must_be_aligned():
                                  1 << 40, FAKE, stream=0, check=False, flags=flags) == K.KVQ_ERR_INVALID_ARG
         assert K.kvq_prefix_attn(desc(), FAKE, 8, 16, FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, 256, FAKE, 2, FAKE, 2, FAKE,
                                  128, 0.1, FAKE, 1 << 40, FAKE, stream=0, check=False, flags=flags) == K.KVQ_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ calls without work
+
+def test_calls_without_work_need_no_buffers():
+    # the address of a tensor without elements is 0
+    none = [None] * 4
+    assert K.kvq_plan_step(0, 64, 8, 4, 16, None, None, FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, FAKE, 256, stream=0,
+                           check=False) == K.KVQ_OK
+    for n, batch, q, lens in ((0, 2, None, FAKE), (8, 0, FAKE, None), (0, 0, None, None)):
+        assert K.kvq_prompt_attn(desc(), q, n, 16, FAKE, FAKE, FAKE, FAKE, None, 4, lens, 256, FAKE, batch, 1, 0.1, FAKE,
+                                 256, q, stream=0, check=False) == K.KVQ_OK
+    assert K.kvq_prefix_attn(desc(), None, 0, 16, *none, None, 4, None, 256, None, 1, None, 4, None, 128, 0.1, None, 0, None,
+                             stream=0, check=False) == K.KVQ_OK
+    # what is wrong about them is still refused
+    assert K.kvq_prompt_attn(desc(), None, 0, 18, *none, None, 4, None, 256, None, 0, 1, 0.1, None, 0, None, stream=0,
+                             check=False) == K.KVQ_ERR_INVALID_ARG
