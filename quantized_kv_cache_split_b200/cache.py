@@ -56,8 +56,7 @@ class QuantizedKVCache:
         self._ws = None
         self._index = _cuda_index(self.device)
         self._ws_rows = {}       # prompt and prefix attention: a workspace per stream
-        self._ws_old = []        # outgrown ones: a captured graph may still use them
-        self._rows_bytes = {}    # workspace bytes by request shape
+        self._rows_bytes = {}    # workspace bytes of recent request shapes
         self._flags = torch.zeros(256, dtype=torch.uint8, device=self.device)  # their flag word
         _settle(self.device)
 
@@ -140,6 +139,8 @@ class QuantizedKVCache:
         key = (kind,) + args
         nbytes = self._rows_bytes.get(key)
         if nbytes is None:
+            if len(self._rows_bytes) >= 64:
+                self._rows_bytes.clear()
             nbytes = self._rows_bytes[key] = size_fn(self.desc, *args)
         if torch._C._cuda_isCurrentStreamCapturing():
             # the graph's own memory: no other graph and no later call uses it
@@ -147,9 +148,11 @@ class QuantizedKVCache:
         else:
             ws = self._ws_rows.get(stream)
             if ws is None or ws.numel() < nbytes:
-                if ws is not None:
-                    self._ws_old.append(ws)
-                ws = self._ws_rows[stream] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+                # an outgrown one goes back to its stream's memory; a quarter more than it, so that
+                # slowly growing requests do not ask for another each time
+                size = max(nbytes, 256, 0 if ws is None else ws.numel() * 5 // 4)
+                self._ws_rows[stream] = ws = None
+                ws = self._ws_rows[stream] = torch.empty(size, dtype=torch.uint8, device=self.device)
         return ws, out, out_type, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale, stream
 
     def prompt_attention(self, q: torch.Tensor, token_offsets: torch.Tensor, seq_lens: torch.Tensor,

@@ -228,3 +228,21 @@ def test_calls_without_work():
     p.free_count.fill_(4)
     p.step(dev([0, 0]), table, p.seq_lens, dev([0, 1, 2, 3]), p.free_count)
     assert p.device_flags() == 0 and c.device_flags() == 0
+
+
+# ------------------------------------------------------------------ memory that a cache keeps
+
+def test_workspaces_do_not_pile_up():
+    # prompts of rising length: the rotated format's partials are the largest
+    pool = Pool("lut4", 64, 1, 64, 40, seed=48)
+    q = dev(pool.queries(1600, 8), np.float16)
+    table = dev([np.arange(40)])
+    out = torch.zeros(1600, 8, 64, device="cuda")
+    torch.cuda.synchronize()
+    start = torch.cuda.memory_allocated()
+    for n in range(1200, 1602, 2):
+        pool.cache.prompt_attention(q[:n], dev([0, n]), dev([n]), n, table, 40, out=out[:n])
+    torch.cuda.synchronize()
+    import quantized_kv_cache_split_b200 as K
+    assert torch.cuda.memory_allocated() - start < 2 * K.kvq_prompt_workspace_size(pool.cache.desc, 1600, 8, 1, 1600)
+    assert len(pool.cache._rows_bytes) <= 64
