@@ -79,6 +79,23 @@ void set_partials(RowsArgs* r, uint8_t* at) {
   r->part_l = r->part_m + n;
 }
 
+// The lengths and offsets that no unit of a prefix decode looks at, because a bound of 0 leaves the
+// prefixes (no row tiles) or the requests' own positions (no own units) without one.
+__global__ void __launch_bounds__(256) check_kernel(const RowsArgs r, const OwnArgs own) {
+  auto bad_len = [&](int len, int most, int pages) {
+    return len < 0 || len > most || len > (int64_t)pages * r.desc.page_size;
+  };
+  bool bad = false;
+  if (r.row_tiles == 0)
+    for (int g = threadIdx.x; g < r.num_groups; g += 256) {
+      const int first = r.offsets ? r.offsets[g] : 0, end = r.offsets ? r.offsets[g + 1] : r.n_tokens;
+      bad |= first < 0 || end < first || end > r.n_tokens || bad_len(r.lens[g], r.max_len, r.max_pages);
+    }
+  if (own.units == 0)
+    for (int b = threadIdx.x; b < r.n_tokens; b += 256) bad |= bad_len(own.seq_lens[b], own.max_seq_len, own.max_pages);
+  if (bad) set_flag(r.flags, KVQ_FLAG_BAD_SEQLEN);
+}
+
 // The calls of the same names; flags: the device flag word, null for the workspace's.
 int prompt_attn(const kvq_cache_desc* desc, const void* q, int32_t n_tokens,
                 int32_t num_q_heads, const void* k_codes, const void* k_scales,
@@ -203,6 +220,10 @@ int prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, int32_
   own.part_m = own.part_o + n_own * desc->head_dim;
   own.part_l = own.part_m + n_own;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (r.row_tiles == 0 || own.units == 0) {
+    check_kernel<<<1, 256, 0, s>>>(r, own);
+    if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
+  }
   st = launch_rows(r, own, s);
   if (st != KVQ_OK) return st;
   return launch_rows_merge(r, own, out, out_type == KVQ_OUT_F16, s);

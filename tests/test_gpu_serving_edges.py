@@ -246,3 +246,26 @@ def test_workspaces_do_not_pile_up():
     import quantized_kv_cache_split_b200 as K
     assert torch.cuda.memory_allocated() - start < 2 * K.kvq_prompt_workspace_size(pool.cache.desc, 1600, 8, 1, 1600)
     assert len(pool.cache._rows_bytes) <= 64
+
+
+# ------------------------------------------------------------------ lengths above a bound of zero
+
+def test_prefix_lengths_above_zero_bounds_set_flags():
+    import quantized_kv_cache_split_b200 as K
+    pool = Pool("q8_0", 64, 1, 64, 8, seed=47)
+    q, tab, own = dev(pool.queries(3, 2), np.float16), dev([[0, 1], [2, 3]]), dev([[4], [5], [6]])
+    call = lambda c, off, plens, pmax, lens, omax: c.prefix_attention(  # noqa: E731
+        q, tab, dev(plens), pmax, dev(lens), omax, own, 1, group_offsets=dev(off))
+    for off, plens, pmax, lens, omax, flag in (
+            ([0, 2, 3], [100, 7], 128, [5, 0, 9], 64, 0), ([0, 2, 3], [0, 0], 0, [5, 0, 9], 64, 0),
+            ([0, 2, 3], [0, 0], 0, [0, 0, 0], 0, 0),
+            ([0, 2, 3], [0, 5], 0, [5, 0, 9], 64, K.KVQ_FLAG_BAD_SEQLEN),       # a prefix above a bound of 0
+            ([0, 3, 3], [0, -1], 0, [5, 0, 9], 64, K.KVQ_FLAG_BAD_SEQLEN),      # of a group without requests
+            ([0, 2, 1], [0, 0], 0, [5, 0, 9], 64, K.KVQ_FLAG_BAD_SEQLEN),       # offsets that fall
+            ([0, 2, 4], [0, 0], 0, [5, 0, 9], 64, K.KVQ_FLAG_BAD_SEQLEN),       # and leave the batch
+            ([-1, 2, 3], [0, 0], 0, [5, 0, 9], 64, K.KVQ_FLAG_BAD_SEQLEN),
+            ([0, 2, 3], [100, 7], 128, [0, 5, 0], 0, K.KVQ_FLAG_BAD_SEQLEN),    # own positions above a bound of 0
+            ([0, 2, 3], [0, 0], 0, [0, 0, -1], 0, K.KVQ_FLAG_BAD_SEQLEN)):
+        cache = K.QuantizedKVCache("q8_0", 64, 1, 64, 8)
+        call(cache, off, plens, pmax, lens, omax)
+        assert cache.device_flags() == flag, (off, plens, pmax, lens, omax)
