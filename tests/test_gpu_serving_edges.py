@@ -269,3 +269,46 @@ def test_prefix_lengths_above_zero_bounds_set_flags():
         cache = K.QuantizedKVCache("q8_0", 64, 1, 64, 8)
         call(cache, off, plens, pmax, lens, omax)
         assert cache.device_flags() == flag, (off, plens, pmax, lens, omax)
+
+
+# ------------------------------------------------------------------ NaN in positions that are seen
+
+def set_nan(pool, position, plane):
+    """A NaN scale at a slot, in every format (0xff bytes: fp16, e4m3 and fp32 NaN)."""
+    t = getattr(pool.cache, plane)
+    t[position // pool.ps, :, position % pool.ps].view(torch.uint8).fill_(0xff)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("plane", ["k_scales", "v_scales"])
+@pytest.mark.parametrize("fmt", FMTS)
+# one piece of one row tile, of two; pieces that the merge joins; a single position
+@pytest.mark.parametrize("n,tokens,at", [(400, 20, 333), (400, 20, 150), (400, 200, 3), (400, 200, 300), (5000, 3, 4700), (1, 1, 0)])
+def test_prompt_nan_reaches_every_row_that_sees_it(fmt, plane, n, tokens, at):
+    pool = Pool(fmt, 64, 1, 64, 80, seed=41)
+    q = dev(pool.queries(tokens, 4), np.float16)
+    args = (dev([0, tokens]), dev([n]), n, dev([np.arange(80)]), 80)
+    clean = pool.cache.prompt_attention(q, *args)
+    set_nan(pool, at, plane)
+    out = pool.cache.prompt_attention(q, *args)
+    sees = torch.arange(tokens, device="cuda") + n - tokens >= at
+    assert torch.isnan(out[sees]).all()
+    if plane == "k_scales":   # (a V that is not finite may reach tokens before it)
+        assert torch.equal(out[~sees], clean[~sees])
+
+
+@pytest.mark.parametrize("plane", ["k_scales", "v_scales"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("where", ["prefix", "own"])
+def test_prefix_nan_reaches_every_request_that_sees_it(fmt, plane, where):
+    pool = Pool(fmt, 64, 1, 64, 40, seed=42)
+    q = dev(pool.queries(3, 4), np.float16)
+    args = (q, dev([np.arange(30)]), dev([1900]), 1920, dev([100, 0, 70]), 128, dev([[30, 31], [32, 33], [34, 35]]), 2)
+    clean = pool.cache.prefix_attention(*args)
+    assert torch.isfinite(clean).all()
+    set_nan(pool, 1234 if where == "prefix" else 34 * 64 + 69, plane)
+    out = pool.cache.prefix_attention(*args)
+    if where == "prefix":
+        assert torch.isnan(out).all()
+    else:
+        assert torch.isnan(out[2]).all() and torch.equal(out[:2], clean[:2])
