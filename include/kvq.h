@@ -397,6 +397,8 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  * 2^7 times their share of a maximum or more: each is off by at most 2^-11 of itself or 2^-32 of
  * the largest); scores, softmax statistics and sums are fp32.  Results do not depend on timing: the same
  * call gives the same bits.
+ * Scores sm_scale q.k up to 2^27 in magnitude are taken as fp32 holds them; beyond, a row may come
+ * out not finite (its weights leave fp16).
  * A NaN in K or V at a position makes NaN of every token that sees the position; an infinity or a
  * NaN in V also of tokens of the same request before it.
  * Same limits as kvq_decode_attn (KVQ_MAX_GROUP, KVQ_MAX_BATCH); lengths up to 2^29.

@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const RowsArgs a, con
         // padding between them), each copied out by the thread that owns it
         uint8_t* mine = smem + S::kQ + (s * 128 + r) * (D * 4 + 16);
         if (a.out) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN stays one)
+          const float inv = row_scale(l, m == -INFINITY);
           f0 *= inv;
           f1 *= inv;
         } else if (write) {

@@ -2,6 +2,8 @@
 // partials (kvq_rows_merge.cu).
 #pragma once
 
+#include <math.h>
+
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -78,6 +80,14 @@ __host__ __device__ inline int row_limit(int len, int n, int i, int causal) {
   if (!causal) return len;
   const int lim = len - n + i + 1;
   return lim < 0 ? 0 : lim;
+}
+
+// What a row of weights summing to l is multiplied by; empty: no maximum, so no position.  The
+// largest weight of any other row is 2^7 or more: a sum below 1 means that the weights have left
+// fp16 downwards (scores beyond 2^27, where fp32 has steps of 8 and more), a NaN that a score was
+// one; neither may pass for a result.
+__device__ __forceinline__ float row_scale(float l, bool empty) {
+  return l >= 1.f ? 1.f / l : empty && l == 0.f ? 0.f : NAN;
 }
 
 }  // namespace kvq

@@ -115,13 +115,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergeArgs
   float acc[E], den = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (M == -INFINITY) M = 0.f;  // nothing to weigh, but a NaN in a sum still counts
+  const bool empty = M == -INFINITY;
+  if (empty) M = 0.f;  // nothing to weigh, but a NaN in a sum still counts
   add_partials<E>(r.part_o + row * r.splits * D, pm, r.part_l + row * r.splits, ns, M, m0, lane, acc, den);
   add_partials<E>(a.own.part_o + row * a.own.max_splits * D, om, a.own.part_l + row * a.own.max_splits, no, M, m1,
                   lane, acc, den);
 #pragma unroll
   for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  const float inv = den == 0.f ? 0.f : 1.f / den;  // (a NaN stays one)
+  const float inv = row_scale(den, empty);
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] *= inv;
   if constexpr (ROT) {

@@ -312,3 +312,36 @@ def test_prefix_nan_reaches_every_request_that_sees_it(fmt, plane, where):
         assert torch.isnan(out).all()
     else:
         assert torch.isnan(out[2]).all() and torch.equal(out[:2], clean[:2])
+
+
+# ------------------------------------------------------------------ scores far beyond ordinary ones
+
+@pytest.mark.parametrize("sm_scale", [1.0, 0.1, -0.1, 0.002])
+@pytest.mark.parametrize("tokens", [3, 40, 200])
+def test_prompt_huge_scores(tokens, sm_scale):
+    # queries and keys of thousands.  Keys are equal within a stretch (so their scores are too) and
+    # the stretches' scores lie thousands apart: the answer is the mean of V over the best stretch
+    # that a row sees.  With sm_scale 1 the scores pass 2^27 (up to 6e8): right or not finite.
+    n, D, G = 700, 64, 4
+    pool = Pool("q8_0", D, 1, 64, 11, seed=43)
+    rng = pool.rng
+    level = np.repeat([508.0, 1016.0, 254.0, 2032.0, 127.0, 1524.0, 63.5], 100)   # 127 * scale, exact
+    k = np.broadcast_to(level[:, None, None], (n, 1, D)).astype(np.float16)
+    v = rng.integers(-127, 128, (n, 1, D)).astype(np.float16)
+    v[:, :, 0::32] = 127.0                                                   # scale 1: exact
+    fill(pool, k, v)
+    assert np.array_equal(pool.v[:n], v.astype(np.float64))
+    q = (rng.uniform(0.5, 1.5, (tokens, G, 1)) * rng.integers(500, 3000, (tokens, G, 1))
+         * rng.choice([-1.0, 1.0], (tokens, G, 1)) * np.ones(D)).astype(np.float16)
+    out = pool.cache.prompt_attention(dev(q, np.float16), dev([0, tokens]), dev([n]), n, dev([np.arange(11)]), 11,
+                                      sm_scale=sm_scale).cpu().numpy().astype(np.float64)
+    for i in range(tokens):
+        seen = n - tokens + i + 1
+        for h in range(G):
+            s = level[:seen] * np.sign(q[i, h, 0]) * np.sign(sm_scale)
+            want = pool.v[:seen][s == s.max(), 0].mean(0)
+            # equal weights, whose sum is taken before their common rounding to fp16 (2^-11), and
+            # fp32 sums
+            right = np.abs(out[i, h] - want).max() <= 127 * (2.0 ** -11 + 2.0 ** -16)
+            assert right or sm_scale == 1.0 and not np.isfinite(out[i, h]).all(), (i, h)
+    assert pool.cache.device_flags() == 0
