@@ -347,4 +347,5 @@ class PagePlanner:
 
     def device_flags(self) -> int:
         """KVQ_FLAG_* bits of the steps so far (a flagged step changed nothing)."""
+        torch.cuda.synchronize(self._index)  # the steps' streams
         return kb.kvq_read_device_flags(self._ws)

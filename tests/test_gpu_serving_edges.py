@@ -345,3 +345,23 @@ def test_prompt_huge_scores(tokens, sm_scale):
             right = np.abs(out[i, h] - want).max() <= 127 * (2.0 ** -11 + 2.0 ** -16)
             assert right or sm_scale == 1.0 and not np.isfinite(out[i, h]).all(), (i, h)
     assert pool.cache.device_flags() == 0
+
+
+# ------------------------------------------------------------------ flags of steps on another stream
+
+def test_planner_flags_wait_for_the_steps_stream():
+    import quantized_kv_cache_split_b200 as K
+    p = K.PagePlanner(2, 64, 8, 2, 16)
+    table, free, count = dev([[0, -1], [1, -1]]), dev(np.arange(8)), dev([4])
+    new, lens = dev([1, 1]), dev([5, 7])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1000)
+        p.step(new, table, lens, free, count)        # the kernels are loaded now
+    lens[1] = -1
+    torch.cuda.synchronize()
+    assert p.device_flags() == 0
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)               # a tenth of a second
+        p.step(new, table, lens, free, count)
+    assert p.device_flags() == K.KVQ_FLAG_BAD_SEQLEN
