@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from tests.serving_helpers import Pool, check_close  # noqa: E402
+from tests.test_gpu_serving import run_prefix, run_prompt  # noqa: E402
 
 FMTS = ["q8_0", "q4_0", "lut4", "nvfp4"]
 
@@ -365,3 +366,82 @@ def test_planner_flags_wait_for_the_steps_stream():
         torch.cuda._sleep(200_000_000)               # a tenth of a second
         p.step(new, table, lens, free, count)
     assert p.device_flags() == K.KVQ_FLAG_BAD_SEQLEN
+
+
+# ------------------------------------------------------------------ many groups, split along their positions
+
+@pytest.mark.parametrize("groups", [33, 40, 70])
+@pytest.mark.parametrize("fmt", ["q8_0", "lut4"])
+def test_prompt_many_groups_of_several_pieces(fmt, groups):
+    # more groups than lanes of a warp, few enough units that positions are split: the fixed chunk,
+    # the search for a block's group and the merge over the pieces; long requests beside short ones,
+    # requests without tokens and without positions
+    import quantized_kv_cache_split_b200 as K
+    pool = Pool(fmt, 64, 1, 64, 420, seed=50)
+    old, new = pool.rng.integers(0, 130, groups), pool.rng.integers(0, 4, groups)
+    for b, n in ((0, 3000), (groups // 2, 1025), (groups - 2, 2047), (groups - 1, 1500)):
+        old[b] = n
+    new[[0, groups // 2, groups - 1]] = 2, 70, 1
+    old[5], new[5] = -1, 2                     # the first of its tokens sees nothing
+    old[6], new[6] = 0, 0
+    rows, longest = int(new.sum()) + 3, int((old + new).max())
+    one = 256 + rows * 4 * (64 + 2) * 4        # a workspace of one piece
+    assert K.kvq_prompt_workspace_size(pool.cache.desc, rows, 4, groups, longest) > one
+    run_prompt(pool, 4, old, new, pad=3, causal=False, half=False, poison=False)
+    run_prompt(pool, 4, old, new, pad=3)       # (leaves NaN in the slots of no request)
+
+
+@pytest.mark.parametrize("fmt", ["q4_0", "lut4"])
+def test_prefix_many_groups_of_several_pieces(fmt):
+    import quantized_kv_cache_split_b200 as K
+    pool = Pool(fmt, 64, 1, 64, 420, seed=51)
+    groups = 40
+    prefix, sizes = pool.rng.integers(0, 130, groups), pool.rng.integers(0, 3, groups)
+    prefix[[0, 7, 20, 39]] = 3000, 0, 1500, 2047
+    sizes[[0, 7, 20, 39]] = 3, 2, 40, 1
+    B = int(sizes.sum())
+    own = pool.rng.integers(0, 60, B)
+    d = pool.cache.desc
+    # more than one piece of the prefixes beside the own part's (that of a short prefix has one)
+    assert K.kvq_prefix_workspace_size(d, B, 4, groups, 3000, 60) > K.kvq_prefix_workspace_size(d, B, 4, groups, 100, 60)
+    run_prefix(pool, 4, [int(n) for n in prefix], [int(n) for n in sizes], [int(n) for n in own])
+
+
+# ------------------------------------------------------------------ bad pages, lengths and offsets of a prefix decode
+
+@pytest.mark.parametrize("groups", [2, 40])
+def test_prefix_bad_pages_and_lengths_set_flags(groups):
+    """In bounds whatever the tables hold: the flags say so (a search finds the group of more than
+    32)."""
+    import quantized_kv_cache_split_b200 as K
+    pool = Pool("q8_0", 64, 1, 64, 8, seed=52)
+    B = groups + 1
+    q = dev(pool.queries(B, 2), np.float16)
+    at = groups - 1                                     # the group and the request that are wrong
+    for what, flag in (("nothing", 0), ("prefix page", K.KVQ_FLAG_BAD_PAGE), ("prefix page -1", K.KVQ_FLAG_BAD_PAGE),
+                       ("own page", K.KVQ_FLAG_BAD_PAGE), ("own page -1", K.KVQ_FLAG_BAD_PAGE),
+                       ("prefix long", K.KVQ_FLAG_BAD_SEQLEN), ("prefix -1", K.KVQ_FLAG_BAD_SEQLEN),
+                       ("own long", K.KVQ_FLAG_BAD_SEQLEN), ("own -1", K.KVQ_FLAG_BAD_SEQLEN),
+                       ("offset -1", K.KVQ_FLAG_BAD_SEQLEN), ("offset falls", K.KVQ_FLAG_BAD_SEQLEN),
+                       ("offset leaves", K.KVQ_FLAG_BAD_SEQLEN)):
+        ptab, plens = np.tile([0, 1, 2], (groups, 1)), np.full(groups, 150)
+        tab, lens, off = np.tile([3, 4], (B, 1)), np.full(B, 100), np.arange(groups + 1)
+        off[-1] = B
+        if "prefix page" in what:
+            ptab[at, 1] = -1 if "-1" in what else 8
+        elif "own page" in what:
+            tab[at, 1] = -1 if "-1" in what else 8
+        elif "prefix" in what:
+            plens[at] = -1 if "-1" in what else 193
+        elif "own" in what:
+            lens[at] = -1 if "-1" in what else 129
+        elif what == "offset -1":
+            off[0] = -1
+        elif what == "offset falls":
+            off[at] = B - 3 if groups > 2 else 0
+            off[at - 1] = B - 2 if groups > 2 else 1
+        elif what == "offset leaves":
+            off[-1] = B + 1
+        cache = K.QuantizedKVCache("q8_0", 64, 1, 64, 8)
+        out = cache.prefix_attention(q, dev(ptab), dev(plens), 192, dev(lens), 128, dev(tab), 2, group_offsets=dev(off))
+        assert out.shape == q.shape and cache.device_flags() == flag, what
