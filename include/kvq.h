@@ -342,6 +342,9 @@ int kvq_noalloc_read_flags(uint32_t* flags, void* stream);
  *                token in its sequence, 0 behind the last one
  *   workspace    device, >= 256 bytes, 16-byte aligned, initialized once with
  *                kvq_workspace_init; only its flag word is used
+ * A request keeps its pages until it ends.  To take tokens back (proposed ones that were rejected),
+ * push the pages behind the first ceil(n / page_size) of the shortened length n on the stack and
+ * raise the count before the next step: lowering seq_lens alone loses them.
  * A step that cannot be done changes nothing but entries of free_pages above the count: it
  * sets a flag (KVQ_FLAG_BAD_SEQLEN: n_b < 0, a_b < -1 or n_b + a_b > max_pages * page_size;
  * KVQ_FLAG_BAD_PAGE: a page id outside [0, num_pages) among the pages that the step moves or
@@ -373,6 +376,9 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  *   every position.)
  * Any number of tokens per request; for a batch of single tokens kvq_decode_attn is the
  * faster call (here the rows of every request take a tensor-core tile of 128).
+ * How the work is cut follows max_seq_len (and for kvq_prefix_attn max_prefix_len), not the lengths
+ * on the device: a bound of four times the lengths costs two to three times the time where few
+ * rows read long caches.  Pass the nearest bound that the host knows.
  *   q            device fp16 [n_tokens][num_q_heads][head_dim], 16-byte aligned: the new tokens
  *                of all requests, packed
  *   token_offsets device int32 [batch + 1], not decreasing, in [0, n_tokens]: request b's
@@ -397,6 +403,8 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  * 2^7 times their share of a maximum or more: each is off by at most 2^-11 of itself or 2^-32 of
  * the largest); scores, softmax statistics and sums are fp32.  Results do not depend on timing: the same
  * call gives the same bits.
+ * kvq_decode_attn multiplies q8_0 and q4_0 codes exactly and scales afterwards, so the same request
+ * comes out closer there (these calls: 4e-4 to 9e-4 of an output's norm).
  * Scores sm_scale q.k up to 2^27 in magnitude are taken as fp32 holds them; beyond, a row may come
  * out not finite (its weights leave fp16).
  * A NaN in K or V at a position makes NaN of every token that sees the position; an infinity or a
@@ -442,6 +450,17 @@ int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, in
                     int32_t max_pages, const int32_t* seq_lens, int32_t max_seq_len, float sm_scale,
                     void* workspace, size_t workspace_bytes, void* out, int32_t out_type,
                     void* stream);
+
+/*
+ * kvq_packed_call -- kvq_plan_step (which = 0), kvq_prompt_attn (1) or kvq_prefix_attn (2) with its
+ * arguments in one block of 64-bit words, for bindings whose cost per argument counts (ctypes: a
+ * third of a microsecond each).
+ *   words   host: the call's arguments in order, pointers and integers as they are, sm_scale as the
+ *           bits of a double; for 1 and 2 one word more, the device address of a 32-bit word in
+ *           which KVQ_FLAG_* bits are set instead of in the workspace's (4-byte aligned, cleared by
+ *           the caller), or 0.  With one, the workspace needs no kvq_workspace_init.
+ */
+int kvq_packed_call(int32_t which, const int64_t* words);
 
 /*
  * kvq_lloyd_max_codebook -- the minimum-MSE `levels`-entry scalar codebook for

@@ -296,6 +296,13 @@ def _word(t) -> int:
         return t or 0
 
 
+def kvq_packed_call(which: int, words: bytes, check: bool = True) -> int:
+    st = _lib.kvq_packed_call(int(which), words)
+    if check:
+        _check("kvq_packed_call", st)
+    return st
+
+
 def kvq_plan_step(batch: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int,
                   seq_lens, new_lens, free_pages, free_count, page_table, seq_lens_out,
                   free_count_out, token_offsets, slots, positions, workspace, workspace_bytes: int,

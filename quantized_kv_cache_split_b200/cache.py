@@ -169,6 +169,9 @@ class QuantizedKVCache:
         padding and keep what ``out`` holds there.  Lengths, offsets and the table are int32
         tensors on the cache's GPU.
 
+        ``max_seq_len`` bounds the lengths, and how the work is cut follows it: pass the nearest
+        bound that the host knows (a quarter of it used costs up to three times the time).
+
         ``stream`` (a torch stream or a handle): launch there instead of on the current stream.
         The inputs must be ready for it and stay alive until the call has run; a new output
         belongs to that stream's memory, so wait for the stream before using it elsewhere.

@@ -315,9 +315,6 @@ int kvq_prefix_attn(const kvq_cache_desc* desc, const void* q, int32_t batch, in
                      sm_scale, workspace, workspace_bytes, out, out_type, nullptr, stream);
 }
 
-// The three calls above from one block of 64-bit words, in their arguments' order (pointers and
-// integers as they are, a float as a double's bits): for bindings whose cost per argument counts.
-// The attention calls take one word more at the end: the device flag word, 0 for the workspace's.
 int kvq_packed_call(int32_t which, const int64_t* w) {
   if (!w) return KVQ_ERR_INVALID_ARG;
   auto ptr = [&](int i) { return reinterpret_cast<void*>(static_cast<uintptr_t>(w[i])); };

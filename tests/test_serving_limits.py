@@ -56,3 +56,11 @@ def test_calls_without_work_need_no_buffers():
     # what is wrong about them is still refused
     assert K.kvq_prompt_attn(desc(), None, 0, 18, *none, None, 4, None, 256, None, 0, 1, 0.1, None, 0, None, stream=0,
                              check=False) == K.KVQ_ERR_INVALID_ARG
+
+
+def test_packed_call_refuses_what_it_does_not_know():
+    assert K.kvq_packed_call(3, b"\0" * 256, check=False) == K.KVQ_ERR_INVALID_ARG
+    assert K.kvq_packed_call(1, None, check=False) == K.KVQ_ERR_INVALID_ARG
+    assert K.kvq_packed_call(1, b"\0" * 256, check=False) == K.KVQ_ERR_INVALID_ARG   # no descriptor
+    with pytest.raises(K.KvqError):
+        K.kvq_packed_call(-1, b"\0" * 256)
