@@ -445,3 +445,36 @@ def test_prefix_bad_pages_and_lengths_set_flags(groups):
         cache = K.QuantizedKVCache("q8_0", 64, 1, 64, 8)
         out = cache.prefix_attention(q, dev(ptab), dev(plens), 192, dev(lens), 128, dev(tab), 2, group_offsets=dev(off))
         assert out.shape == q.shape and cache.device_flags() == flag, what
+
+
+# ------------------------------------------------------------------ a captured plan of two launches
+
+def test_captured_large_plan_replays():
+    # more than 65,536 slots: the slots come from a second launch, scheduled early; the state stays
+    # on the GPU and moves on with each replay
+    import quantized_kv_cache_split_b200 as K
+    from tests.serving_helpers import plan_reference
+    B, ps, mp, num_pages, cap = 40, 64, 30, 1300, 70001
+    p = K.PagePlanner(B, ps, num_pages, mp, cap)
+    rng = np.random.Generator(np.random.PCG64(53))
+    table, free = torch.full((B, mp), -1, dtype=torch.int32, device="cuda"), dev(rng.permutation(num_pages))
+    p.free_count.fill_(num_pages)
+    new = dev(rng.integers(0, 300, B))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        p.step(new, table, p.seq_lens, free, p.free_count)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.step(new, table, p.seq_lens, free, p.free_count)
+    for turn in range(5):
+        new.copy_(dev(np.where(rng.random(B) < 0.3, -1, rng.integers(0, 300, B))))
+        was = [t.cpu().numpy() for t in (p.seq_lens, new, free, p.free_count, table)]
+        want = plan_reference(was[0], was[1], was[2], int(was[3][0]), was[4], ps, cap)
+        graph.replay()
+        assert p.device_flags() == 0
+        assert np.array_equal(table.cpu().numpy(), want["table"])
+        assert np.array_equal(free.cpu().numpy()[:len(want["stack"])], want["stack"])
+        for name, t in (("lens", p.seq_lens), ("offsets", p.token_offsets), ("slots", p.slots), ("positions", p.positions)):
+            assert np.array_equal(t.cpu().numpy(), want[name]), (turn, name)
