@@ -398,13 +398,13 @@ size_t kvq_prefix_workspace_size(const kvq_cache_desc* desc, int32_t batch, int3
  *                not overlap on the GPU.
  *   out          device [n_tokens][num_q_heads][head_dim] of out_type, 16-byte aligned
  *   out_type     KVQ_OUT_F32 or KVQ_OUT_F16 (one rounding of the fp32 result)
- * Roundings: K and V values to fp16 once dequantized (nvfp4: first the block scale times the
- * vector scale; lut4: the rotated query as well), the weights to fp16 for the product with V (as
- * 2^7 times their share of a maximum or more: each is off by at most 2^-11 of itself or 2^-32 of
- * the largest); scores, softmax statistics and sums are fp32.  Results do not depend on timing: the same
- * call gives the same bits.
+ * Roundings: K and V values to fp16 once dequantized (once each), the rotated lut4 query, and the
+ * weights for the product with V (as 2^7 times their share of a maximum or more: each is off by at
+ * most 2^-11 of itself or 2^-32 of the largest); scores, softmax statistics and sums are fp32.
+ * Results do not depend on timing: the same call gives the same bits.
  * kvq_decode_attn multiplies q8_0 and q4_0 codes exactly and scales afterwards, so the same request
- * comes out closer there (these calls: 4e-4 to 9e-4 of an output's norm).
+ * comes out closer there (these calls: 3e-4 to 1e-3 of an output's norm, the most for keys with
+ * high scores over long caches).
  * Scores sm_scale q.k up to 2^27 in magnitude are taken as fp32 holds them; beyond, a row may come
  * out not finite (its weights leave fp16).
  * A NaN in K or V at a position makes NaN of every token that sees the position; an infinity or a

@@ -99,15 +99,15 @@ __device__ __forceinline__ void own_v(const uint8_t* __restrict__ codes, const u
       const int o = C::RAWB * r;
       return codes + slot * C::CROW + (((o >> 4) ^ swz<FMT, D>(slot)) << 4) + (o & 15);
     };
-    auto scale = [&](int slot) -> __half {
-      if (slot >= n_valid) return __ushort_as_half(0);
+    auto scale = [&](int slot) -> float {
+      if (slot >= n_valid) return 0.f;
       const uint8_t* srow = scales + slot * C::SROW;
-      if constexpr (C::kNv)
-        return __float2half_rn(e4m3_float(srow[C::E * r / 16]) * *reinterpret_cast<const float*>(srow + D / 16));
-      return *reinterpret_cast<const __half*>(srow);
+      if constexpr (C::kNv) return e4m3_float(srow[C::E * r / 16]) * *reinterpret_cast<const float*>(srow + D / 16);
+      return __half2float(*reinterpret_cast<const __half*>(srow));
     };
     const int sa = s0 + 2 * c, sc = sa + 8;
-    const __half2 dab = __halves2half2(scale(sa), scale(sa + 1)), dcd = __halves2half2(scale(sc), scale(sc + 1));
+    const float fa = scale(sa), fb = scale(sa + 1), fc = scale(sc), fd = scale(sc + 1);
+    const __half2 dab = __floats2half2_rn(fa, fb), dcd = __floats2half2_rn(fc, fd);
     uint32_t wa[C::NWORD], wb[C::NWORD], e[2][C::E];
     v_raw<FMT, D>(code(sa), wa);
     v_raw<FMT, D>(code(sa + 1), wb);
@@ -115,16 +115,24 @@ __device__ __forceinline__ void own_v(const uint8_t* __restrict__ codes, const u
     v_raw<FMT, D>(code(sc), wa);
     v_raw<FMT, D>(code(sc + 1), wb);
     v_dequant_pair<FMT, D>(wa, wb, lut, e[1]);
-    // nvfp4: halved (exact), so that no value passes the fp16 range
-    const __half2 half = u32_as_h2(C::kNv ? 0x38003800u : 0x3C003C00u);
+    if constexpr (C::kNv) {
+      // halved (exact), so that no value passes the fp16 range; what the rounded scale leaves of
+      // the exact one is added before the product is rounded
+      const __half2 half = u32_as_h2(0x38003800u);
+      const float2 ab = __half22float2(dab), cd = __half22float2(dcd);
+      const __half2 lab = __floats2half2_rn(fa - ab.x, fb - ab.y), lcd = __floats2half2_rn(fc - cd.x, fd - cd.y);
 #pragma unroll
-    for (int i = 0; i < C::E; ++i) {
-      if constexpr (C::kNv) {
-        e[0][i] = hmul2u(e[0][i], half);
-        e[1][i] = hmul2u(e[1][i], half);
+      for (int i = 0; i < C::E; ++i) {
+        const __half2 x = __hmul2(u32_as_h2(e[0][i]), half), y = __hmul2(u32_as_h2(e[1][i]), half);
+        e[0][i] = h2_as_u32(__hfma2(x, dab, __hmul2(x, lab)));
+        e[1][i] = h2_as_u32(__hfma2(y, dcd, __hmul2(y, lcd)));
       }
-      e[0][i] = hmul2u(e[0][i], dab);
-      e[1][i] = hmul2u(e[1][i], dcd);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C::E; ++i) {
+        e[0][i] = hmul2u(e[0][i], dab);
+        e[1][i] = hmul2u(e[1][i], dcd);
+      }
     }
 #pragma unroll
     for (int mt = 0; mt < C::MT; ++mt) mma16816(acc[mt], e[0][2 * mt], e[0][2 * mt + 1], e[1][2 * mt], e[1][2 * mt + 1], p01, p89);

@@ -24,8 +24,7 @@
 //
 // Own positions of prefix decode are units of one warp (kvq_own.cuh) in blocks of the same grid.
 //
-// Roundings: K and V values to fp16 (2^-11 relative, as code * scale; nvfp4 first its block scale
-// times vector scale), the lut4 query after its rotation to fp16, the weights to fp16: the
+// Roundings: K and V values to fp16 once (2^-11 relative, as code * scale), the lut4 query after its rotation to fp16, the weights to fp16: the
 // operand types of the tensor core.  Scores, maxima, sums and accumulators are fp32.
 //
 // What bounds it.  256 rows x 128 positions at head_dim 128: the MMAs alone 2048 clocks, the
@@ -114,8 +113,9 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int c) {
 }
 
 // ------------------------------------------------------------------ dequantization
+// lo (nvfp4): what the scale d leaves of its exact value, so that a product is rounded once.
 template <int FMT, int D>
-__device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, __half2 d, const Lut& lut) {
+__device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, __half2 d, __half2 lo, const Lut& lut) {
   using C = Cfg<FMT, D>;
   uint4 r;
   if constexpr (C::kQ8) {
@@ -139,8 +139,12 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, __half2 d, c
     uint32_t L0, H0, L1, H1;
     lut_lookup4(lut, w0, nib_mask_lo(w0), L0, H0);
     lut_lookup4(lut, w0 >> 16, nib_mask_hi(w0), L1, H1);
-    r = make_uint4(hmul2u(prmt(L0, H0, 0x5140u), d), hmul2u(prmt(L0, H0, 0x7362u), d),
-                   hmul2u(prmt(L1, H1, 0x5140u), d), hmul2u(prmt(L1, H1, 0x7362u), d));
+    auto two = [&](uint32_t x) {
+      if constexpr (C::kNv) return h2_as_u32(__hfma2(u32_as_h2(x), d, __hmul2(u32_as_h2(x), lo)));
+      return hmul2u(x, d);
+    };
+    r = make_uint4(two(prmt(L0, H0, 0x5140u)), two(prmt(L0, H0, 0x7362u)), two(prmt(L1, H1, 0x5140u)),
+                   two(prmt(L1, H1, 0x7362u)));
   }
   return r;
 }
@@ -172,7 +176,7 @@ __device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8
   };
   // every load first: the stores below might alias them for all the compiler knows
   uint4 u[kTasks];
-  __half2 d[kTasks][C::kNv ? 2 : 1];
+  __half2 d[kTasks][C::kNv ? 2 : 1], lo[kTasks][C::kNv ? 2 : 1];
 #pragma unroll
   for (int i = 0; i < kTasks; ++i) {
     int row, j;
@@ -183,8 +187,12 @@ __device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8
     if constexpr (C::kNv) {
       const uint32_t e = lds16(sp + 2 * j);
       const float g = *reinterpret_cast<const float*>(sp + D / 16);
-      d[i][0] = __float2half2_rn(live ? e4m3_float(e & 0xffu) * g : 0.f);
-      d[i][1] = __float2half2_rn(live ? e4m3_float(e >> 8) * g : 0.f);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float x = live ? e4m3_float(e >> (8 * k) & 0xffu) * g : 0.f;
+        d[i][k] = __float2half2_rn(x);
+        lo[i][k] = __float2half2_rn(x - __low2float(d[i][k]));
+      }
     } else {
       const uint32_t b = lds16(sp + (C::kQ8 ? j >> 1 : C::kQ4 ? j : 0) * 2);
       d[i][0] = __half2half2(__ushort_as_half((unsigned short)(live ? b : 0u)));
@@ -198,8 +206,9 @@ __device__ __forceinline__ void fill_half(const uint8_t* __restrict__ raw, uint8
     constexpr int kOut = C::kQ8 ? 2 : 4;  // 16-byte chunks of eight values
 #pragma unroll
     for (int c = 0; c < kOut; ++c) {
-      const uint4 v = C::kQ8 ? dequant8<FMT, D>(w[2 * c & 3], w[(2 * c + 1) & 3], d[i][0], lut)
-                             : dequant8<FMT, D>(w[c], 0u, d[i][C::kNv ? c >> 1 : 0], lut);
+      const int b = C::kNv ? c >> 1 : 0;
+      const uint4 v = C::kQ8 ? dequant8<FMT, D>(w[2 * c & 3], w[(2 * c + 1) & 3], d[i][0], d[i][0], lut)
+                             : dequant8<FMT, D>(w[c], 0u, d[i][b], lo[i][b], lut);
       *reinterpret_cast<uint4*>(tile + tile_offset(row0 + row, kOut * j + c)) = v;
     }
   }

@@ -478,3 +478,57 @@ def test_captured_large_plan_replays():
         assert np.array_equal(free.cpu().numpy()[:len(want["stack"])], want["stack"])
         for name, t in (("lens", p.seq_lens), ("offsets", p.token_offsets), ("slots", p.slots), ("positions", p.positions)):
             assert np.array_equal(t.cpu().numpy(), want[name]), (turn, name)
+
+
+# ------------------------------------------------------------------ one rounding of a K or V value
+
+U = 2.0 ** -11 * (1 + 2.0 ** -9)   # half a step of fp16, and what fp32 adds
+
+
+def requests_of(fmt, n, positions, seed):
+    """n requests of a page each with the given K and V rows [n, positions, 1, D]."""
+    pool = Pool(fmt, 64, 1, 64, n, seed=seed)
+    return pool, np.arange(n)[:, None] * 64 + np.arange(positions)
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0", "nvfp4"])
+@pytest.mark.parametrize("op", ["prompt", "own"])
+def test_values_are_rounded_once(fmt, op):
+    # a single position has weight 1 exactly: the answer is V as it enters the product
+    n = 300
+    pool, slots = requests_of(fmt, n, 1, 54)
+    q, lens, table = dev(pool.queries(n, 2), np.float16), dev([1] * n), dev(np.arange(n).reshape(n, 1))
+    if op == "prompt":
+        out = pool.cache.prompt_attention(q, dev(np.arange(n + 1)), lens, 64, table, 1)
+    else:
+        out = pool.cache.prefix_attention(q, dev([[0]]), dev([0]), 64, lens, 64, table, 1)
+    want = np.repeat(pool.v[slots[:, 0]], 2, 1)
+    err = np.abs(out.cpu().numpy() - want)
+    assert (err <= np.abs(want) * U + 2.0 ** -24).all(), float((err / np.maximum(np.abs(want) * U, 1e-30)).max())
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0", "nvfp4"])
+def test_keys_are_rounded_once(fmt):
+    # two positions, K 0 and V 0 at the first, K the same c in every dimension and V 1 at the second:
+    # the answer is the second's weight, 1 / (1 + e^-s), from which the score's error shows.  The
+    # roundings of equal K values are equal and add up.
+    n, D = 300, 64
+    pool, slots = requests_of(fmt, n, 2, 55)
+    rng = pool.rng
+    k = np.zeros((n, 2, 1, D), dtype=np.float16)
+    k[:, 1] = rng.uniform(0.5, 2.0, (n, 1, 1))
+    k[:, 1, 0, ::16] *= rng.uniform(1.0, 3.0, (n, 1))          # other block and vector scales
+    v = np.zeros((n, 2, 1, D), dtype=np.float16)
+    v[:, 1] = 1.0
+    pool.cache.write(dev(k.reshape(-1, 1, D), np.float16), dev(v.reshape(-1, 1, D), np.float16), dev(slots.reshape(-1)))
+    torch.cuda.synchronize()
+    pool.k, pool.v = pool.values("k"), pool.values("v")
+    q = np.full((n, 1, D), 0.25, dtype=np.float16)
+    out = pool.cache.prompt_attention(dev(q, np.float16), dev(np.arange(n + 1)), dev([2] * n), 64,
+                                      dev(np.arange(n).reshape(n, 1)), 1).cpu().numpy().astype(np.float64)
+    s = (0.25 / math.sqrt(D)) * pool.k[slots[:, 1], 0].sum(-1)
+    w = 1 / (1 + np.exp(-s))
+    got = (out[:, 0] / pool.v[slots[:, 1], 0]).mean(-1)
+    # V is rounded too (its error is the same in every dimension); w' = w (1 - w)
+    assert (np.abs(got - w) <= w * (1 - w) * s * U * (1 + s * U) + w * 2.0 ** -20 + w * np.abs(
+        np.float64(np.float16(pool.v[slots[0, 1], 0, 0] / 2)) * 2 - pool.v[slots[0, 1], 0, 0])).all()
