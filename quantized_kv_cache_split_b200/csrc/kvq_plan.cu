@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(const PlanArgs a) {
 int launch_plan(const PlanArgs& a, cudaStream_t stream) {
   // Up to kSmallStep slots one CTA (256 tokens: 7 us), then a cluster of eight (37,000 slots: 12 us),
   // then the cluster for the pages and a second launch, scheduled early, for the slots (494,000
-  // slots: 10 us, against 26 by the cluster alone; the launch itself costs the host 5).
+  // slots: 10 us, against 26 by the cluster alone; the launch itself costs the host 5).  Where the
+  // two routes cross between 37,000 and 494,000 was not measured.
   const bool apart = (int64_t)a.max_tokens > kLargeStep;
   const int ctas = (int64_t)a.max_tokens > kSmallStep ? kPlanCluster : 1;
   cudaLaunchConfig_t cfg = {};

@@ -24,18 +24,19 @@
 //
 // Own positions of prefix decode are units of one warp (kvq_own.cuh) in blocks of the same grid.
 //
-// Roundings: K and V values to fp16 once (2^-11 relative, as code * scale), the lut4 query after its rotation to fp16, the weights to fp16: the
-// operand types of the tensor core.  Scores, maxima, sums and accumulators are fp32.
+// Roundings: K and V values to fp16 once (2^-11 relative, as code * scale), the lut4 query after
+// its rotation to fp16, the weights to fp16: the operand types of the tensor core.  Scores, maxima,
+// sums and accumulators are fp32.
 //
 // What bounds it.  256 rows x 128 positions at head_dim 128: the MMAs alone 2048 clocks, the
 // exponentials alone 2048 (16 a clock and SM), shared memory about 2600 (the fp16 tiles written
 // and read by the MMAs, the query read again for every tile, the staged codes); measured 3900.
 // Both streams alternate: one's weights are computed while the other's MMAs run.  Measured on a
-// 64K q8_0 prefix for 256 requests (32/4 heads, 275 GFLOP): 290 us alone, 950 TFLOP/s, 330 in a
-// sustained loop under the power cap; tensor pipe 56 % busy on the SMs at work, exponentials 57 %,
-// issue slots 60 %.  Tried and slower there: 64-position tiles with two score buffers per stream
-// (345 us), two threads per row (370, register spills), a quarter of the exponentials on the FMA
-// pipe (358), a pass for the tile's maximum (321).
+// 64K q8_0 prefix for 256 requests (32/4 heads, 275 GFLOP): 332 to 340 us back to back, 810 to 830
+// TFLOP/s, at 1807 MHz under the power cap; tensor pipe 55 % busy on the SMs at work, exponentials
+// 56 %, issue slots 60 %.  Tried and slower there, when a single launch took 291: 64-position tiles
+// with two score buffers per stream (345 us), two threads per row (370, register spills), a quarter
+// of the exponentials on the FMA pipe (358), a pass for the tile's maximum (321).
 // 128 rows or fewer: 2550 clocks for 128 positions, bound by dequantizing through shared memory.
 #include <math.h>
 
@@ -62,7 +63,8 @@ static_assert(32 * (kOwnWarps * kOwnRegs + (kThreads / 32 - kOwnWarps) * kMmaReg
 // long tail of small weights is not lost to rounding (with one bit of headroom 64K positions 2^-26
 // below the maximum, 0.1 % of the sum, vanished from the product while the denominator counted
 // them), and its normal range reaches 2^-21 below.  A tile of equal scores sums to 2^14, half of
-// kSafeSum; a maximum may grow 2^1 to 2^8 times before it has to be raised.
+// kSafeSum; a maximum may grow 2^1 to 2^8 times before it has to be raised.  (That bit less headroom
+// costs 1 % of the 8K prompt and 3 % of the ragged ones.)
 constexpr float kWeightBits = 7.f;
 constexpr float kSafeSum = 32768.f;  // a tile's weights summing to less are all inside fp16
 constexpr uint32_t kTmemColumns = 512;

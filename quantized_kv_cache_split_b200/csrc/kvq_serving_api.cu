@@ -33,9 +33,10 @@ bool needs_merge(const kvq_cache_desc* desc, const RowsPlan& p) {
 }
 
 // How prompt attention is cut.  Up to 512 positions in one piece, written to the output directly:
-// the merge costs more than the split saves (512 positions, 200 tokens of 32 heads: 20.7 us against
-// 24.8; at 1024 positions the split wins, 22.8 against 25.6 for 64 tokens).  lut4 output goes
-// through the merge in any case and keeps its splits.
+// the merge costs more than the split saves (200 tokens of 32 heads at 512 positions: 20.3 us against
+// 24.9; from 1 to 8 requests of 1 to 200 tokens at 300 to 512 positions 2 to 7 us less or the same;
+// at 1024 positions the split wins, 22.8 against 25.6 for 64 tokens).  lut4 output goes through the
+// merge in any case and keeps its splits.
 RowsPlan plan_prompt(const kvq_cache_desc* desc, int n_tokens, int num_q_heads, int batch, int max_seq_len) {
   RowsPlan p = plan_rows(desc->num_kv_heads, num_q_heads / desc->num_kv_heads, n_tokens, batch, max_seq_len, kTargetCtas);
   if (max_seq_len <= 4 * kKvTile && desc->fmt != KVQ_FMT_LUT4) {
