@@ -93,7 +93,8 @@ class QuantizedKVCache:
         sequence and KV head).  ``v_fetch``: how V rows reach the SM when tau > 0:
         "kept" (only the kept rows, after the skip test), "with_k" (every V tile with its
         K tile; skipped rows are left out of the contraction only) or "auto" (with_k);
-        the result is the same.  ``stream``: as for prompt_attention."""
+        the result is the same.  ``stream``: as for prompt_attention.  Make one call of a shape
+        before capturing it: the workspace is cleared when it is made."""
         other = _elsewhere(stream, self._index)
         if other is not None:
             return _run_on(other, self._index, out, self.attention, q, seq_lens, max_seq_len, page_table, max_pages, tau,
